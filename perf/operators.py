@@ -357,6 +357,9 @@ def _own(s):
     import microscaling_weight_quantization_amd as mxq
     case = s["case"]
     kind, fp8 = case["kind"], torch.float8_e4m3fn
+    out = {}
+    if "out" in case:    # bf16 results take the matrix cores' own FP8 sums, fp32 results sums in fp32
+        out = {"out_dtype": DTYPES[case["out"]], "fast_accum": case["out"] == "bf16"}
     if kind == "quantize":
         if case["cols"]:
             q, codes, col, col_codes = mxq.mxq_quantize_fp8_group128_row_col(s["x"])
@@ -364,13 +367,11 @@ def _own(s):
         q, codes = mxq.mxq_quantize_fp8_group128(s["x"])
         return {"row": q.view(fp8), "row_codes": codes}
     if kind == "matmul":
-        return mxq.mxq_matmul_fp8_block128(*s["a"], *s["w"], offsets=s["offsets"], out_dtype=DTYPES[case["out"]])
+        return mxq.mxq_matmul_fp8_block128(*s["a"], *s["w"], offsets=s["offsets"], **out)
     if kind == "dgrad":
-        return mxq.mxq_matmul_fp8_block128_dgrad(*s["a"], *s["w"], offsets=s["offsets"],
-                                                 out_dtype=DTYPES[case["out"]])
+        return mxq.mxq_matmul_fp8_block128_dgrad(*s["a"], *s["w"], offsets=s["offsets"], **out)
     if kind == "wgrad":
-        return mxq.mxq_matmul_fp8_group128_wgrad(*s["dy"], *s["x"], offsets=s["offsets"],
-                                                 out_dtype=DTYPES[case["out"]])
+        return mxq.mxq_matmul_fp8_group128_wgrad(*s["dy"], *s["x"], offsets=s["offsets"], **out)
     if kind == "route":
         offsets, slots, position = mxq.mxq_sort_experts(s["ids"], case["experts"])
         out = {"offsets": offsets, "slots": slots, "position": position}
