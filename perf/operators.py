@@ -358,7 +358,7 @@ def _own(s):
     case = s["case"]
     kind, fp8 = case["kind"], torch.float8_e4m3fn
     out = {}
-    if "out" in case:    # bf16 results take the matrix cores' own FP8 sums, fp32 results sums in fp32
+    if "out" in case:    # activations and their gradients in bf16 take the matrix cores' own FP8 sums, others sums in fp32
         out = {"out_dtype": DTYPES[case["out"]], "fast_accum": case["out"] == "bf16"}
     if kind == "quantize":
         if case["cols"]:
@@ -371,7 +371,8 @@ def _own(s):
     if kind == "dgrad":
         return mxq.mxq_matmul_fp8_block128_dgrad(*s["a"], *s["w"], offsets=s["offsets"], **out)
     if kind == "wgrad":
-        return mxq.mxq_matmul_fp8_group128_wgrad(*s["dy"], *s["x"], offsets=s["offsets"], **out)
+        return mxq.mxq_matmul_fp8_group128_wgrad(*s["dy"], *s["x"], offsets=s["offsets"],
+                                                 out_dtype=DTYPES[case["out"]])
     if kind == "route":
         offsets, slots, position = mxq.mxq_sort_experts(s["ids"], case["experts"])
         out = {"offsets": offsets, "slots": slots, "position": position}
