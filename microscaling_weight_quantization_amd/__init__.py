@@ -38,7 +38,11 @@ ENTRY_POINTS = ("mxq_status_string", "mxq_fake_quantize_mxfp4", "mxq_mxfp4_to_mx
                 "mxq_mxfp4_packed_to_mxfp8_row", "mxq_mxfp4_packed_to_fp8_block128", "mxq_mxfp4_to_mxfp8_col",
                 "mxq_mxfp4_to_mxfp8_row_col", "mxq_mxfp4_to_mxfp8_col_guarded", "mxq_mxfp4_to_mxfp8_row_col_guarded",
                 "mxq_mxfp4_to_mxfp8_row_grouped", "mxq_fake_quantize_mxfp4_grouped",
-                "mxq_mxfp4_to_fp8_block128_grouped", "mxq_dequantize_grouped", "mxq_quantize_mxfp4_grouped")
+                "mxq_mxfp4_to_fp8_block128_grouped", "mxq_dequantize_grouped", "mxq_quantize_mxfp4_grouped",
+                "mxq_quantize_fp8_group128", "mxq_quantize_fp8_group128_col", "mxq_quantize_fp8_group128_row_col",
+                "mxq_matmul_fp8_block128", "mxq_matmul_fp8_block128_dgrad", "mxq_matmul_fp8_group128_wgrad",
+                "mxq_sort_experts", "mxq_sort_experts_workspace", "mxq_dispatch_rows", "mxq_combine_rows",
+                "mxq_combine_rows_backward")
 
 _libs = {}
 _lock = threading.Lock()
@@ -114,8 +118,21 @@ def load(name: str = "libmxq.so") -> ctypes.CDLL:
         L.mxq_mxfp4_to_fp8_block128_grouped.argtypes = [ctypes.POINTER(_Block128Group), i64, i32, vp]
         L.mxq_dequantize_grouped.argtypes = [ctypes.POINTER(_DequantGroup), i64, i32, i32, i32, vp]
         L.mxq_quantize_mxfp4_grouped.argtypes = [ctypes.POINTER(_Mxfp4Group), i64, i32, vp]
+        quant = [vp, i64, i64, i64, i64, i32, vp, i64]                  # x, ld, x_rows, rows, K, dtype, slots, top_k
+        L.mxq_quantize_fp8_group128.argtypes = quant + [u8p, i64, u8p, i64, vp]
+        L.mxq_quantize_fp8_group128_col.argtypes = quant + [vp, i64, u8p, i64, u8p, i64, vp]
+        L.mxq_quantize_fp8_group128_row_col.argtypes = quant + [vp, i64] + [u8p, i64] * 4 + [vp]
+        product = [u8p, i64, u8p, i64, u8p, i64, i64, u8p, i64, i64, i64, i64, i64, vp, i64, vp, i64, i32, i32, vp]
+        L.mxq_matmul_fp8_block128.argtypes = product
+        L.mxq_matmul_fp8_block128_dgrad.argtypes = product
+        L.mxq_matmul_fp8_group128_wgrad.argtypes = [u8p, i64] * 4 + [i64, i64, i64, vp, i64, vp, i64, i64, i32, vp]
+        L.mxq_sort_experts.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+        L.mxq_sort_experts_workspace.argtypes = [i64, i64, i64]
+        L.mxq_dispatch_rows.argtypes = [vp, i64, i64, vp, i64, i64, i64, i32, vp, i64, vp]
+        L.mxq_combine_rows.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+        L.mxq_combine_rows_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64, vp, vp]
         for n in ENTRY_POINTS[1:]:
-            getattr(L, n).restype = i32
+            getattr(L, n).restype = i64 if n.endswith("_workspace") else i32
         _libs[name] = L
         return L
 
@@ -685,6 +702,282 @@ def mxq_quantize_mxfp4_grouped(xs, packeds=None, scales=None, scale_ld: Optional
     """Packed MXFP4 (deployment format) of a list of weights of one dtype, in as
     few launches as possible -> (list of nibble pairs, list of E8M0 codes)."""
     return GroupedQuantizeMxfp4(xs, packeds, scales, scale_ld, lib)()
+
+
+# ---- FP8 products and the routing of a layer of experts ------------------------------------
+
+def _ng(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _vector(t: torch.Tensor, n: int, dtype: torch.dtype, what: str) -> int:
+    """Pointer of a contiguous array of n elements of `dtype`."""
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {dtype} tensor of {n} elements, "
+                         f"got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _experts_of(offsets: Optional[torch.Tensor]):
+    """(pointer, number of experts) of an offsets tensor; (None, 0) for None."""
+    if offsets is None:
+        return None, 0
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets is a tensor of n_experts + 1 elements")
+    return _vector(offsets, offsets.shape[0], torch.int32, "offsets"), offsets.shape[0] - 1
+
+
+def _code_rows(rows: int, n_experts: int) -> int:
+    """Code rows of groups of 128 rows: begun anew with each expert, or at row 0."""
+    return rows // 128 + n_experts if n_experts else _ng(rows)
+
+
+def _source(x: torch.Tensor, slots: Optional[torch.Tensor], top_k: int):
+    """The quantizer's leading arguments, and the rows and columns of its result."""
+    px, x_rows, K, ldx = _matrix(x)
+    if slots is None:
+        return (px, ldx, x_rows, x_rows, K, _dtype_code(x), None, 1), x_rows, K
+    rows = slots.numel()
+    return (px, ldx, x_rows, rows, K, _dtype_code(x), _vector(slots, rows, torch.int32, "slots"), top_k), rows, K
+
+
+def _bytes_for(x: torch.Tensor, t: Optional[torch.Tensor], rows: int, cols: int, what: str):
+    """(tensor, pointer, row stride) of a byte output, allocated if missing."""
+    if t is None:
+        t = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        return t, t.data_ptr(), cols
+    p, ld = _operand(t, rows, cols, what, byte=True)
+    return t, p, ld
+
+
+@_device_operands
+def mxq_quantize_fp8_group128(x: torch.Tensor, slots: Optional[torch.Tensor] = None, top_k: int = 1,
+                              data: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                              lib: str = "libmxq.so"):
+    """FP8 payload and E8M0 codes of groups of 128 along the rows of x (bf16 / fp32) ->
+    (payload uint8 [rows, K], codes uint8 [rows, ceil(K/128)]).  With `slots` (int32, as
+    mxq_sort_experts returns them) row r of the result is x's row slots[r] // top_k, zeros for a
+    dropped slot."""
+    L = load(lib)
+    args, rows, K = _source(x, slots, top_k)
+    data, pd, ldd = _bytes_for(x, data, rows, K, "payload")
+    scale, ps, lds = _bytes_for(x, scale, rows, _ng(K), "scale")
+    _check(L, L.mxq_quantize_fp8_group128(*args, pd, ldd, ps, lds, _stream(x)))
+    return data, scale
+
+
+@_device_operands
+def mxq_quantize_fp8_group128_col(x: torch.Tensor, slots: Optional[torch.Tensor] = None, top_k: int = 1,
+                                  offsets: Optional[torch.Tensor] = None, data: Optional[torch.Tensor] = None,
+                                  scale: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """The same with groups of 128 rows of a column, the operand of a weight gradient ->
+    (payload uint8 [rows, K], codes uint8 [groups, K]).  With `offsets` (int32 [n_experts + 1])
+    groups begin anew with each expert's rows and there are rows // 128 + n_experts code rows."""
+    L = load(lib)
+    args, rows, K = _source(x, slots, top_k)
+    po, n = _experts_of(offsets)
+    data, pd, ldd = _bytes_for(x, data, rows, K, "payload")
+    scale, ps, lds = _bytes_for(x, scale, _code_rows(rows, n), K, "scale")
+    _check(L, L.mxq_quantize_fp8_group128_col(*args, po, n, pd, ldd, ps, lds, _stream(x)))
+    return data, scale
+
+
+@_device_operands
+def mxq_quantize_fp8_group128_row_col(x: torch.Tensor, slots: Optional[torch.Tensor] = None, top_k: int = 1,
+                                      offsets: Optional[torch.Tensor] = None,
+                                      row_data: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None,
+                                      col_data: Optional[torch.Tensor] = None, col_scale: Optional[torch.Tensor] = None,
+                                      lib: str = "libmxq.so"):
+    """Groups along the rows and along the columns from one read of x ->
+    (row payload, row codes, column payload, column codes)."""
+    L = load(lib)
+    args, rows, K = _source(x, slots, top_k)
+    po, n = _experts_of(offsets)
+    row_data, prd, ldrd = _bytes_for(x, row_data, rows, K, "row payload")
+    row_scale, prs, ldrs = _bytes_for(x, row_scale, rows, _ng(K), "row_scale")
+    col_data, pcd, ldcd = _bytes_for(x, col_data, rows, K, "column payload")
+    col_scale, pcs, ldcs = _bytes_for(x, col_scale, _code_rows(rows, n), K, "col_scale")
+    _check(L, L.mxq_quantize_fp8_group128_row_col(*args, po, n, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs, _stream(x)))
+    return row_data, row_scale, col_data, col_scale
+
+
+def _weights(w: torch.Tensor, tile_code: torch.Tensor, n_experts: int):
+    """(N, K, the C call's arguments) of [N, K] payloads and their tile codes, n_experts of them if not 0."""
+    lead = 3 if n_experts else 2
+    if w.dim() != lead or tile_code.dim() != lead or (n_experts and not w.shape[0] == tile_code.shape[0] == n_experts):
+        raise ValueError("w and tile_code are [N, K] and [ceil(N/128), ceil(K/128)], with offsets [n_experts, ...] "
+                         f"of them; got {list(w.shape)} and {list(tile_code.shape)}")
+    if w.element_size() != 1 or tile_code.element_size() != 1:
+        raise ValueError(f"w and tile_code hold bytes, got {w.dtype} and {tile_code.dtype}")
+    N, K = w.shape[-2:]
+    tr, tc = _ng(N), _ng(K)
+    if tile_code.shape[-2] < tr or tile_code.shape[-1] < tc:
+        raise ValueError(f"tile_code must cover [{tr}, {tc}], got {list(tile_code.shape)}")
+    if (K > 1 and w.stride(-1) != 1) or (tc > 1 and tile_code.stride(-1) != 1):
+        raise ValueError("the last dimension must be contiguous")
+    return N, K, (w.data_ptr(), w.stride(-2) if N > 1 else K, w.stride(0) if n_experts else 0, tile_code.data_ptr(),
+                  tile_code.stride(-2) if tr > 1 else tc, tile_code.stride(0) if n_experts else 0)
+
+
+def _rows_operand(t: torch.Tensor, scale: torch.Tensor, cols: int, what: str):
+    """(rows, the C call's arguments) of a payload [rows, cols] with row groups."""
+    p, rows, tcols, ld = _matrix(t)
+    if tcols != cols or t.element_size() != 1:
+        raise ValueError(f"{what} holds bytes, [rows, {cols}], got {t.dtype} {list(t.shape)}")
+    ps, lds = _operand(scale, rows, _ng(cols), what + "_scale", byte=True)
+    return rows, (p, ld, ps, lds)
+
+
+def _result(like: torch.Tensor, out: Optional[torch.Tensor], shape, out_dtype: torch.dtype):
+    """(tensor, pointer, row stride, stride of a leading dimension, dtype) of an output, allocated if missing."""
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=like.device)
+    elif tuple(out.shape) != tuple(shape):
+        raise ValueError(f"the output is {list(shape)}, got {list(out.shape)}")
+    if shape[-1] > 1 and out.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return out, out.data_ptr(), out.stride(-2) if shape[-2] > 1 else shape[-1], out.stride(0), _dtype_code(out)
+
+
+@_device_operands
+def mxq_matmul_fp8_block128(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, tile_code: torch.Tensor,
+                            offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                            out_dtype: torch.dtype = torch.bfloat16, fast_accum: bool = False,
+                            lib: str = "libmxq.so") -> torch.Tensor:
+    """y = x w^T in FP8: x [M, K] with its codes [M, ceil(K/128)] (mxq_quantize_fp8_group128), w [N, K]
+    with its tile codes (mxq_mxfp4_to_fp8_block128) -> [M, N] bf16 / fp32.  With `offsets` (int32
+    [n_experts + 1]) the rows of x are sorted by expert, w is [n_experts, N, K] and expert e's rows
+    meet w[e]; rows of no expert give zeros.  Products are summed in fp32; with `fast_accum` the FP8
+    matrix instructions sum them, at about twice the rate and up to 2^-10 of the sum of magnitudes off."""
+    L = load(lib)
+    po, n = _experts_of(offsets)
+    N, K, pw = _weights(w, tile_code, n)
+    M, px = _rows_operand(x, x_scale, K, "x")
+    out, py, ldy, _, dt = _result(x, out, (M, N), out_dtype)
+    _check(L, L.mxq_matmul_fp8_block128(*px, *pw, M, N, K, po, n, py, ldy, dt, fast_accum, _stream(x)))
+    return out
+
+
+@_device_operands
+def mxq_matmul_fp8_block128_dgrad(dy: torch.Tensor, dy_scale: torch.Tensor, w: torch.Tensor, tile_code: torch.Tensor,
+                                  offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                  out_dtype: torch.dtype = torch.bfloat16, fast_accum: bool = False,
+                                  lib: str = "libmxq.so") -> torch.Tensor:
+    """dx = dy w in FP8, the input's gradient of mxq_matmul_fp8_block128: dy [M, N] with its codes
+    [M, ceil(N/128)], the same w and tile codes -> [M, K]."""
+    L = load(lib)
+    po, n = _experts_of(offsets)
+    N, K, pw = _weights(w, tile_code, n)
+    M, pg = _rows_operand(dy, dy_scale, N, "dy")
+    out, px, ldx, _, dt = _result(dy, out, (M, K), out_dtype)
+    _check(L, L.mxq_matmul_fp8_block128_dgrad(*pg, *pw, M, N, K, po, n, px, ldx, dt, fast_accum, _stream(dy)))
+    return out
+
+
+@_device_operands
+def mxq_matmul_fp8_group128_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                                  offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                  out_dtype: torch.dtype = torch.float32, lib: str = "libmxq.so") -> torch.Tensor:
+    """dw = dy^T x in FP8, the weight's gradient: dy [M, N] and x [M, K] with the codes of column groups
+    (mxq_quantize_fp8_group128_col, both with the same `offsets`) -> [N, K], or [n_experts, N, K]."""
+    L = load(lib)
+    po, n = _experts_of(offsets)
+    pg, M, N, ldg = _matrix(dy)
+    px, mx, K, ldx = _matrix(x)
+    if mx != M or dy.element_size() != 1 or x.element_size() != 1:
+        raise ValueError(f"dy and x hold bytes and have the same rows, got {dy.dtype} {list(dy.shape)} and "
+                         f"{x.dtype} {list(x.shape)}")
+    groups = _code_rows(M, n)
+    pgs, ldgs = _operand(dy_scale, groups, N, "dy_scale", byte=True)
+    pxs, ldxs = _operand(x_scale, groups, K, "x_scale", byte=True)
+    out, pw, ldw, stride, dt = _result(dy, out, (n, N, K) if n else (N, K), out_dtype)
+    _check(L, L.mxq_matmul_fp8_group128_wgrad(pg, ldg, pgs, ldgs, px, ldx, pxs, ldxs, M, N, K, po, n, pw, ldw, stride,
+                                              dt, _stream(dy)))
+    return out
+
+
+@_device_operands
+def mxq_sort_experts(ids: torch.Tensor, n_experts: int, lib: str = "libmxq.so"):
+    """Slots of ids (int32 [tokens, top_k], the experts of each token) sorted by expert, stably ->
+    (offsets [n_experts + 1], slots [tokens * top_k], position [tokens, top_k]), all int32.  Expert e
+    owns sorted rows offsets[e] .. offsets[e + 1]; slots[r] is the slot of sorted row r and
+    position[t, j] the sorted row of slot t * top_k + j.  Ids outside [0, n_experts) are dropped:
+    their slots come last and both directions hold the complement."""
+    L = load(lib)
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError(f"ids is int32 [tokens, top_k], got {ids.dtype} {list(ids.shape)}")
+    pi, T, k, ldi = _matrix(ids)
+    need = L.mxq_sort_experts_workspace(T, k, n_experts)
+    # one allocation: offsets, slots, position, workspace
+    n = T * k
+    buf = torch.empty(n_experts + 1 + 2 * n + need // 4, dtype=torch.int32, device=ids.device)
+    at = buf.data_ptr()
+    a, b = n_experts + 1, n_experts + 1 + n
+    _check(L, L.mxq_sort_experts(pi, ldi, T, k, n_experts, at, at + 4 * a, at + 4 * b, at + 4 * (b + n), need,
+                                 _stream(ids)))
+    return buf[:a], buf[a:b], buf[b:b + n].view(T, k)
+
+
+@_device_operands
+def mxq_dispatch_rows(x: torch.Tensor, slots: torch.Tensor, top_k: int, out: Optional[torch.Tensor] = None,
+                      lib: str = "libmxq.so") -> torch.Tensor:
+    """x's rows (bf16 / fp32 [tokens, H]) in sorted order: row r is x[slots[r] // top_k], zeros for a
+    dropped slot -> [slots, H].  Its gradient is mxq_combine_rows without weights."""
+    L = load(lib)
+    px, T, H, ldx = _matrix(x)
+    rows = slots.numel()
+    ps = _vector(slots, rows, torch.int32, "slots")
+    out, po, ldo, _, dt = _result(x, out, (rows, H), x.dtype)
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's dtype")
+    _check(L, L.mxq_dispatch_rows(px, ldx, T, ps, rows, top_k, H, dt, po, ldo, _stream(x)))
+    return out
+
+
+def _slots_of(position: torch.Tensor, weights: Optional[torch.Tensor]):
+    if position.dim() != 2:
+        raise ValueError(f"position is int32 [tokens, top_k], got {list(position.shape)}")
+    T, k = position.shape
+    return (T, k, _vector(position, T * k, torch.int32, "position"),
+            None if weights is None else _vector(weights, T * k, torch.float32, "weights"))
+
+
+@_device_operands
+def mxq_combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, lib: str = "libmxq.so") -> torch.Tensor:
+    """Sorted rows (bf16 / fp32 [rows, H]) back to their tokens: y[t] = sum over j of weights[t, j] *
+    rows[position[t, j]] -> [tokens, H].  `weights` fp32 [tokens, top_k], None: all 1."""
+    L = load(lib)
+    pr, R, H, ldr = _matrix(rows)
+    T, k, pp, pw = _slots_of(position, weights)
+    out, py, ldy, _, dt = _result(rows, out, (T, H), rows.dtype)
+    if out.dtype != rows.dtype:
+        raise ValueError("out must have the rows' dtype")
+    _check(L, L.mxq_combine_rows(pr, ldr, R, pp, pw, T, k, H, dt, py, ldy, _stream(rows)))
+    return out
+
+
+@_device_operands
+def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: torch.Tensor,
+                              weights: Optional[torch.Tensor] = None, drows: Optional[torch.Tensor] = None,
+                              dweights: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """Gradients of mxq_combine_rows for dy [tokens, H] -> (drows [rows, H], dweights fp32 [tokens, top_k]).
+    `position` names every row once, as mxq_sort_experts returns it."""
+    L = load(lib)
+    pg, T0, H, ldg = _matrix(dy)
+    pr, R, hr, ldr = _matrix(rows)
+    T, k, pp, pw = _slots_of(position, weights)
+    if (T0, hr) != (T, H) or dy.dtype != rows.dtype:
+        raise ValueError(f"dy is [tokens, H] of the rows' dtype, got {dy.dtype} {list(dy.shape)} for "
+                         f"{T} tokens and rows {rows.dtype} {list(rows.shape)}")
+    drows, pd, ldd, _, dt = _result(dy, drows, (R, H), rows.dtype)
+    if drows.dtype != rows.dtype:
+        raise ValueError("drows must have the rows' dtype")
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    pv = _vector(dweights, T * k, torch.float32, "dweights")
+    _check(L, L.mxq_combine_rows_backward(pg, ldg, pr, ldr, R, pp, pw, T, k, H, dt, pd, ldd, pv, _stream(dy)))
+    return drows, dweights
 
 
 # ---- convenience layer ------------------------------------------------------------------

@@ -5,7 +5,9 @@
 the build-variant tests: ``libmxq_fastmath.so`` (fast-math, denormals flushed),
 ``libmxq_o1.so`` (-O1) and ``libmxq_o0.so`` (-O0, no optimisation).  Every
 step of the path is integer arithmetic, so all four builds must produce
-identical bits.  ``libmxq_shapes.so`` holds the access-shape reference kernels
+identical bits.  The FP8 products, their quantizer and the expert routing
+(``OBJECTS``) are compiled once, with -O3, and linked into all four.
+``libmxq_shapes.so`` holds the access-shape reference kernels
 (``csrc/shapes.hip``) that bench.py times beside the library's kernels.
 """
 from __future__ import annotations
@@ -21,8 +23,8 @@ SRC = os.path.join(HERE, "csrc", "mxq.hip")
 INCLUDE = os.path.join(ROOT, "include")
 ARCH = "gfx950"
 
-# Packed fp32 instructions are kept out of every build; the library has no fp32 math anyway.
-COMMON = ["--offload-arch=" + ARCH, "-std=c++17", "-fPIC", "-shared", "-Wall",
+# Packed fp32 instructions are kept out of every build.
+COMMON = ["--offload-arch=" + ARCH, "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-I" + INCLUDE]
 
 VARIANTS = {
@@ -32,6 +34,8 @@ VARIANTS = {
     "libmxq_o0.so": ["-O0"],
     "libmxq_shapes.so": ["-O3"],
 }
+OBJECTS = ("group_quant", "product", "experts")
+OBJECT_HEADERS = ("checks.h", "segments.h", "fastdiv.h")
 SOURCES = {"libmxq_shapes.so": os.path.join(HERE, "csrc", "shapes.hip")}   # the others: SRC
 
 
@@ -42,10 +46,9 @@ def hipcc() -> str:
     return "hipcc"
 
 
-def build_one(name: str, flags, verbose: bool = False) -> str:
-    out = os.path.join(HERE, name)
+def _compile(out: str, args, verbose: bool) -> str:
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [hipcc()] + COMMON + flags + [SOURCES.get(name, SRC), "-o", tmp]
+    cmd = [hipcc()] + COMMON + args + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
@@ -53,10 +56,25 @@ def build_one(name: str, flags, verbose: bool = False) -> str:
     return out
 
 
+def object_source(name: str) -> str:
+    return os.path.join(HERE, "csrc", name + ".hip")
+
+
+def build_object(name: str, verbose: bool = False) -> str:
+    return _compile(os.path.join(HERE, name + ".o"), ["-O3", "-c", object_source(name)], verbose)
+
+
+def build_one(name: str, flags, verbose: bool = False, objects=()) -> str:
+    if name in SOURCES:
+        return _compile(os.path.join(HERE, name), ["-shared"] + flags + [SOURCES[name]], verbose)
+    return _compile(os.path.join(HERE, name), ["-shared"] + flags + list(objects) + [SRC], verbose)   # objects first: hipcc takes what follows a source for one
+
+
 def build(variants=None, verbose: bool = False):
     names = list(VARIANTS) if variants is None else list(variants)
-    with ThreadPoolExecutor(len(names)) as ex:
-        return list(ex.map(lambda n: build_one(n, VARIANTS[n], verbose), names))
+    with ThreadPoolExecutor(max(len(names), len(OBJECTS))) as ex:
+        objects = list(ex.map(lambda n: build_object(n, verbose), OBJECTS)) if any(n not in SOURCES for n in names) else []
+        return list(ex.map(lambda n: build_one(n, VARIANTS[n], verbose, objects), names))
 
 
 def library_path(name: str = "libmxq.so") -> str:
@@ -68,7 +86,11 @@ def stale(name: str = "libmxq.so") -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    srcs = (SOURCES[name], os.path.join(INCLUDE, "mxq_shapes.h")) if name in SOURCES else (SRC, os.path.join(INCLUDE, "mxq.h"))
+    if name in SOURCES:
+        srcs = (SOURCES[name], os.path.join(INCLUDE, "mxq_shapes.h"))
+    else:
+        srcs = (SRC, os.path.join(INCLUDE, "mxq.h"), *(object_source(n) for n in OBJECTS),
+                *(os.path.join(HERE, "csrc", h) for h in OBJECT_HEADERS))
     return any(os.path.getmtime(p) > t for p in srcs)
 
 
