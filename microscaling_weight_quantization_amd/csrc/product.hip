@@ -88,21 +88,23 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* p, int avail) {
 // A tile of X rows (of V or U) by kR of the reduction in LDS, in 16-byte chunks.
 // kContig: [X][kR], chunk c of row x at place c ^ (x / 2 % 8): the 16 rows that a
 // wave's lanes read at once then fall on all 64 banks.  Else [kR][X], chunk c of
-// row r at place c ^ (r % 8), for the same reason.
+// row r at place c ^ (r % 8) (rows of 64 bytes: c ^ (r / 4 % 4)), for the same
+// reason: 16 lanes read one chunk of 8 consecutive rows.
 template <bool kContig, int X, int kThreads>
 struct Tile {
   static constexpr int kChunks = X * kR / 16 / kThreads;
   static constexpr int kBytes = X * kR;
 
+  // LDS offset of chunk pos of row x (kContig) or r.
+  static __device__ __forceinline__ int at(int row, int pos) {
+    if constexpr (kContig) return row * kR + ((pos ^ ((row >> 1) & 7)) << 4);
+    else if constexpr (X == 64) return row * X + ((pos ^ ((row >> 2) & 3)) << 4);
+    else return row * X + ((pos ^ (row & 7)) << 4);
+  }
   static __device__ __forceinline__ int place(int q) {
     const int c = threadIdx.x + q * kThreads;
-    if constexpr (kContig) {
-      const int x = c / 8, pos = c % 8;
-      return x * kR + ((pos ^ ((x >> 1) & 7)) << 4);
-    } else {
-      const int r = c / (X / 16), pos = c % (X / 16);
-      return r * X + ((pos ^ (r & 7)) << 4);
-    }
+    if constexpr (kContig) return at(c / 8, c % 8);
+    else return at(c / (X / 16), c % (X / 16));
   }
   // Chunk q of this thread: rows x0 .. of at most x_end, reduction r0 .. of at most r_end.
   static __device__ __forceinline__ i32x4 load(const uint8_t* base, int64_t ld, int x0, int x_end, int r0, int r_end,
@@ -121,15 +123,14 @@ struct Tile {
     const int lane = threadIdx.x & 63, g = lane / 16, i = lane % 16;
     i32x8 f;
     if constexpr (kContig) {
-      const int row = x + i, s = (row >> 1) & 7;
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + row * kR + (((2 * g) ^ s) << 4));
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + row * kR + (((2 * g + 1) ^ s) << 4));
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + at(x + i, 2 * g));
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + at(x + i, 2 * g + 1));
       f = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
         const int r = 32 * g + 8 * t + i / 2;
-        const uint8_t* p = lds + r * X + (((x >> 4) ^ (i / 2)) << 4) + (i & 1) * 8;
+        const uint8_t* p = lds + at(r, x >> 4) + (i & 1) * 8;
         const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(MXQ_LDS(i32x2, p));
         f[2 * t] = w[0];
         f[2 * t + 1] = w[1];
@@ -175,6 +176,68 @@ __device__ __forceinline__ Wide widen(i32x8 f) {
       w.v[q][4 * h] = lo[0], w.v[q][4 * h + 1] = lo[1], w.v[q][4 * h + 2] = hi[0], w.v[q][4 * h + 3] = hi[1];
     }
   return w;
+}
+
+// Fragments of V as the products take them.
+template <bool kFast, int N>
+struct Prepared;
+template <int N>
+struct Prepared<true, N> {
+  i32x8 v[N];
+  __device__ __forceinline__ explicit Prepared(const i32x8 (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = f[i];
+  }
+};
+template <int N>
+struct Prepared<false, N> {
+  Wide v[N];
+  __device__ __forceinline__ explicit Prepared(const i32x8 (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = widen(f[i]);
+  }
+};
+
+// Codes of U that one lane needs for rows col .. col + 15: that of its own row
+// (lane % 16) for the scaled product, or those of its four results' rows.
+template <bool kFast>
+struct Codes {
+  int c[kFast ? 1 : 4];
+};
+template <bool kFast>
+__device__ __forceinline__ Codes<kFast> u_codes(const Args& a, const uint8_t* uc, int col, int64_t b) {
+  const int lane = threadIdx.x & 63;
+  Codes<kFast> k;
+#pragma unroll
+  for (int t = 0; t < (kFast ? 1 : 4); t++) {
+    const int j = col + (kFast ? lane % 16 : lane / 16 * 4 + t);
+    k.c[t] = j < a.J ? uc[(j >> a.u.x_shift) * a.u.code_x + b * a.u.code_r] : 127;
+  }
+  return k;
+}
+
+// One reduction block of 16 rows of U times 16 N rows of V, added to acc.
+template <bool kFast, int N>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[N], const Prepared<kFast, N>& v, const int (&cv)[N], i32x8 u,
+                                         const Codes<kFast>& cu) {
+  if constexpr (kFast) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(u, v.v[i], acc[i], 0, 0, 0, cu.c[0], 0, cv[i]);
+  } else {
+    const Wide w = widen(u);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      f32x4 sum{0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; q++) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[q], v.v[i].v[q], sum, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+        const float scaled = __builtin_ldexpf(sum[t], cu.c[t] + cv[i] - 254);
+        acc[i][t] += cu.c[t] == 255 || cv[i] == 255 ? __builtin_nanf("") : scaled;
+      }
+    }
+  }
 }
 
 template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
@@ -229,51 +292,18 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args 
 #pragma unroll
     for (int q = 0; q < TU::kChunks; q++) *reinterpret_cast<i32x4*>(lu + TU::place(q)) = su[q];
     __syncthreads();
-    int cv[WI / 16];   // the codes of this lane's rows i
+    int cv[WI / 16];
+    i32x8 fv[WI / 16];
 #pragma unroll
     for (int i = 0; i < WI / 16; i++) {
       const int row = i0 + wi + 16 * i + lane % 16;
       cv[i] = row < i_end ? vc[row * a.v.code_x + b * a.v.code_r] : 127;
+      fv[i] = TV::fragment(lv, wi + 16 * i);
     }
-    if constexpr (kFast) {
-      i32x8 fv[WI / 16];
+    const Prepared<kFast, WI / 16> pv(fv);
 #pragma unroll
-      for (int i = 0; i < WI / 16; i++) fv[i] = TV::fragment(lv, wi + 16 * i);
-#pragma unroll
-      for (int j = 0; j < WJ / 16; j++) {
-        const int col = j0 + wj + 16 * j + lane % 16;
-        const int cu = col < a.J ? uc[(col >> a.u.x_shift) * a.u.code_x + b * a.u.code_r] : 127;
-        const i32x8 fu = TU::fragment(lu, wj + 16 * j);
-#pragma unroll
-        for (int i = 0; i < WI / 16; i++)
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fu, fv[i], acc[j][i], 0, 0, 0, cu, 0, cv[i]);
-      }
-    } else {
-      Wide fv[WI / 16];
-#pragma unroll
-      for (int i = 0; i < WI / 16; i++) fv[i] = widen(TV::fragment(lv, wi + 16 * i));
-#pragma unroll
-      for (int j = 0; j < WJ / 16; j++) {
-        int cu[4];   // the codes of this lane's four columns j
-#pragma unroll
-        for (int t = 0; t < 4; t++) {
-          const int col = j0 + wj + 16 * j + lane / 16 * 4 + t;
-          cu[t] = col < a.J ? uc[(col >> a.u.x_shift) * a.u.code_x + b * a.u.code_r] : 127;
-        }
-        const Wide fu = widen(TU::fragment(lu, wj + 16 * j));
-#pragma unroll
-        for (int i = 0; i < WI / 16; i++) {
-          f32x4 sum{0, 0, 0, 0};
-#pragma unroll
-          for (int q = 0; q < 4; q++) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fu.v[q], fv[i].v[q], sum, 0, 0, 0);
-#pragma unroll
-          for (int t = 0; t < 4; t++) {
-            const float scaled = __builtin_ldexpf(sum[t], cu[t] + cv[i] - 254);
-            acc[j][i][t] += cu[t] == 255 || cv[i] == 255 ? __builtin_nanf("") : scaled;
-          }
-        }
-      }
-    }
+    for (int j = 0; j < WJ / 16; j++)
+      multiply<kFast>(acc[j], pv, cv, TU::fragment(lu, wj + 16 * j), u_codes<kFast>(a, uc, j0 + wj + 16 * j, b));
   }
 
   TO* const out = reinterpret_cast<TO*>(a.out) + (kMode == kWgrad ? expert * a.out_expert_stride : 0);
@@ -289,8 +319,173 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args 
   }
 }
 
+// ---- few rows -------------------------------------------------------------------------------
+// With few rows i a product is bound by reading U once, so nothing is shared
+// between waves on the way: each of a workgroup's waves takes every kWaves-th
+// reduction block of the same 16 kNJ rows of U, straight from memory to the
+// product instructions, one block ahead of them, and the waves' sums are added
+// through LDS in a fixed order at the end.  Where U's reduction axis is strided
+// (dx), a wave turns its block around in an LDS tile of its own.
+constexpr int kFewWaves = 8;
+
+// Reduction r .. r + 31 of a row, of which the first r_end - r are the operand's.
+__device__ __forceinline__ i32x8 row_fragment(const uint8_t* row, int r, int r_end) {
+  const i32x4 lo = load16(row + r, r_end - r), hi = load16(row + r + 16, r_end - r - 16);
+  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+template <Mode kMode, bool kFast, typename TO, int kNI, int kNJ>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
+  static_assert(kMode != kWgrad, "a weight gradient reduces over the rows");
+  constexpr bool kTurn = kMode == kDgrad;
+  constexpr int BJ = 16 * kNJ, kChunks = BJ * kR / 16 / 64;
+  using T = Tile<false, BJ, 64>;
+  constexpr int kSum = kNI * kNJ * 64 * 4;                       // floats of one wave's sums
+  constexpr int kShared = kFewWaves / 2 * kSum * 4;
+  constexpr int kTurned = kTurn ? kFewWaves * BJ * kR : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kTurned > kShared ? kTurned : kShared];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+  const int j0 = blockIdx.x * BJ;
+  int i0 = blockIdx.y * 16 * kNI, i_end = a.I, blocks = (a.R + kR - 1) / kR, expert = 0;
+  if (a.offsets) {
+    const Segment s = mxq_dev::find_tile<16 * kNI>(a.offsets, a.experts, a.I, blockIdx.y);
+    i0 = min((int64_t)s.lo + (int64_t)s.tile * 16 * kNI, (int64_t)s.hi), i_end = s.hi;
+    if (i0 >= i_end) return;
+    if (s.expert == a.experts) blocks = 0;
+    else expert = s.expert;
+  }
+  const uint8_t* const ud = a.u.data + expert * a.u.expert_stride;
+  const uint8_t* const uc = a.u.code + expert * a.u.code_expert_stride;
+  uint8_t* const tile = lds + wave * BJ * kR;
+
+  // rows past the end read the last one's bytes: what they add is not stored
+  const uint8_t* vrow[kNI];
+  const uint8_t* vcode[kNI];
+#pragma unroll
+  for (int i = 0; i < kNI; i++) {
+    const int row = min(i0 + 16 * i + lane % 16, i_end - 1);
+    vrow[i] = a.v.data + row * a.v.ld;
+    vcode[i] = a.v.code + row * a.v.code_x;
+  }
+  const uint8_t* urow[kNJ];
+  if constexpr (!kTurn) {
+#pragma unroll
+    for (int j = 0; j < kNJ; j++) urow[j] = ud + min(j0 + 16 * j + lane % 16, a.J - 1) * a.u.ld;
+  }
+  const uint8_t* ucode[kNJ];
+#pragma unroll
+  for (int j = 0; j < kNJ; j++) ucode[j] = uc + (min(j0 + 16 * j, a.J - 1) >> 7) * a.u.code_x;
+
+  struct Block {
+    i32x8 v[kNI];
+    int cv[kNI], cu[kNJ];
+    i32x8 u[kTurn ? 1 : kNJ];
+    i32x4 raw[kTurn ? kChunks : 1];
+  };
+  auto load = [&](Block& k, int b) {
+    const int r = b * kR + lane / 16 * 32;
+    if constexpr (kTurn) {
+#pragma unroll
+      for (int q = 0; q < kChunks; q++) {
+        const int c = lane + 64 * q, ur = b * kR + c / kNJ, uj = j0 + c % kNJ * 16;
+        k.raw[q] = load16(ud + ur * a.u.ld + uj, ur < a.R ? a.J - uj : 0);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kNJ; j++) k.u[j] = row_fragment(urow[j], r, a.R);
+    }
+#pragma unroll
+    for (int i = 0; i < kNI; i++) {
+      k.v[i] = row_fragment(vrow[i], r, a.R);
+      k.cv[i] = vcode[i][b];
+    }
+#pragma unroll
+    for (int j = 0; j < kNJ; j++) k.cu[j] = ucode[j][b * a.u.code_r];
+  };
+
+  f32x4 acc[kNJ][kNI];
+#pragma unroll
+  for (int j = 0; j < kNJ; j++)
+#pragma unroll
+    for (int i = 0; i < kNI; i++) acc[j][i] = f32x4{0, 0, 0, 0};
+
+  Block now, next;
+  if (wave < blocks) load(now, wave);
+  for (int b = wave; b < blocks; b += kFewWaves) {
+    if (b + kFewWaves < blocks) load(next, b + kFewWaves);
+    if constexpr (kTurn) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int q = 0; q < kChunks; q++) {
+        const int c = lane + 64 * q;
+        *reinterpret_cast<i32x4*>(tile + T::at(c / kNJ, c % kNJ)) = now.raw[q];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    const Prepared<kFast, kNI> pv(now.v);
+#pragma unroll
+    for (int j = 0; j < kNJ; j++) {
+      Codes<kFast> cu;   // 16 neighbouring columns lie in one tile
+#pragma unroll
+      for (int t = 0; t < (kFast ? 1 : 4); t++) cu.c[t] = now.cu[j];
+      i32x8 u;
+      if constexpr (kTurn) u = T::fragment(tile, 16 * j);
+      else u = now.u[j];
+      multiply<kFast>(acc[j], pv, now.cv, u, cu);
+    }
+    now = next;
+  }
+
+  float* const sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int half = kFewWaves / 2; half >= 1; half /= 2) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int t = 0; t < kNI * kNJ; t++)
+        *reinterpret_cast<f32x4*>(sums + (wave - half) * kSum + (t * 64 + lane) * 4) = acc[t / kNI][t % kNI];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int t = 0; t < kNI * kNJ; t++)
+        acc[t / kNI][t % kNI] += *reinterpret_cast<const f32x4*>(sums + wave * kSum + (t * 64 + lane) * 4);
+    }
+  }
+  if (wave) return;
+  TO* const out = reinterpret_cast<TO*>(a.out);
+#pragma unroll
+  for (int i = 0; i < kNI; i++) {
+    const int row = i0 + 16 * i + lane % 16;
+    if (row >= i_end) continue;
+#pragma unroll
+    for (int j = 0; j < kNJ; j++) {
+      const int col = j0 + 16 * j + lane / 16 * 4;
+      if (col < a.J) store4(out + row * a.ld_out + col, acc[j][i], a.J - col, a.vec_out);
+    }
+  }
+}
+
+template <Mode kMode, bool kFast, typename TO, int kNI, int kNJ>
+int launch_few(const Args& a, hipStream_t stream) {
+  const int64_t tj = ((int64_t)a.J + 16 * kNJ - 1) / (16 * kNJ);
+  const int64_t ti = a.offsets ? a.I / (16 * kNI) + a.experts + 2 : ((int64_t)a.I + 16 * kNI - 1) / (16 * kNI);
+  if (ti > 65535) return MXQ_ERR_SHAPE;
+  hipLaunchKernelGGL((few_rows_kernel<kMode, kFast, TO, kNI, kNJ>), dim3((uint32_t)tj, (uint32_t)ti),
+                     dim3(kFewWaves * 64), 0, stream, a);
+  return launch_status();
+}
+
 template <Mode kMode, bool kFast, typename TO>
 int launch(const Args& a, hipStream_t stream) {
+  if constexpr (kMode != kWgrad) {
+    // rows that meet one weight: all of them, or an expert's share
+    const int64_t rows = a.offsets ? (a.I + a.experts - 1) / a.experts : a.I;
+    if (rows <= 16) return launch_few<kMode, kFast, TO, 1, kMode == kDgrad ? 8 : 4>(a, stream);
+    if (rows <= 32) return launch_few<kMode, kFast, TO, 2, 4>(a, stream);
+    if (rows <= 64) return launch_few<kMode, kFast, TO, 4, 4>(a, stream);
+  }
   constexpr int BI = 128, BJ = 128, WI = 64, WJ = 64;
   const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
   int64_t ti = ((int64_t)a.I + BI - 1) / BI, tz = 1;
