@@ -319,6 +319,277 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args 
   }
 }
 
+// ---- many rows ------------------------------------------------------------------------------
+// Tiles of V and U go from memory to LDS without passing through registers
+// (buffer loads to LDS), one block ahead of the products; one barrier a block.
+// The LDS places of a wave's 64 chunks are consecutive, so the swizzle is applied
+// to the addresses that its lanes read.  A buffer's bound turns reads past the
+// operand's end into zeros.
+//
+// Needs 16-byte aligned rows (and a contiguous axis that ends on a whole chunk).
+
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  return (const T*)uniform((int64_t)p);
+}
+
+// Loads from a buffer to LDS.  A buffer is bytes [base, base + left), at most
+// 2^31 - 1 of them; offsets at or past its end read zeros.  A wave's lanes write
+// consecutive words (or 16 bytes each) from the LDS address `to` on.  These are
+// instructions and not the compiler's builtins, which would wait for them before
+// every later LDS read; they have no output register.  arrive() waits for this
+// wave's and then for the workgroup's.
+constexpr int kPastEnd = 0x7FFFFFFF;
+__device__ __forceinline__ i32x4 buffer(const uint8_t* base, int64_t left) {
+  const uint64_t p = (uint64_t)base;
+  return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32), (int)min(max(left, (int64_t)0), (int64_t)kPastEnd), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+#define MXQ_LOAD_TO_LDS(name, instruction)                                                             \
+  __device__ __forceinline__ void name(i32x4 from, uint32_t to, int off) {                             \
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t" instruction " %0, %1, 0 offen lds" ::"v"(off), "s"(from), "s"(to) \
+                 : "memory", "m0");                                                                    \
+  }
+MXQ_LOAD_TO_LDS(load_to_lds_16, "buffer_load_dwordx4")
+MXQ_LOAD_TO_LDS(load_to_lds_4, "buffer_load_dword")
+MXQ_LOAD_TO_LDS(load_to_lds_1, "buffer_load_ubyte")
+#undef MXQ_LOAD_TO_LDS
+__device__ __forceinline__ void arrive() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <bool kContig, int X, int kThreads>
+struct Feed {
+  using T = Tile<kContig, X, kThreads>;
+  const uint8_t* base;   // row x0, block 0
+  int64_t step;          // bytes from one block to the next
+  int64_t left;          // bytes from base to the operand's end
+  int32_t off[T::kChunks];
+  int32_t r_of_chunk;    // kContig: reduction index within the block, the same for all of this lane's chunks
+
+  // rows x0 .. x_end - 1 (of the axis that the output keeps), reduction r0 .. r_end - 1
+  __device__ __forceinline__ Feed(const uint8_t* data, int64_t ld, int x0, int x_end, int r0, int r_end) {
+    if constexpr (kContig) {
+      base = uniform(data + x0 * ld + r0);
+      step = kR;
+      left = (int64_t)(x_end - x0 - 1) * ld + (r_end - r0);
+    } else {
+      base = uniform(data + r0 * ld + x0);
+      step = kR * ld;
+      left = (int64_t)(r_end - r0 - 1) * ld + (x_end - x0);
+    }
+    left = uniform(left);
+    r_of_chunk = 0;
+#pragma unroll
+    for (int q = 0; q < T::kChunks; q++) {
+      const int c = threadIdx.x + q * kThreads;
+      if constexpr (kContig) {
+        const int x = c / 8, pos = (c % 8) ^ ((x >> 1) & 7);   // x advances by multiples of 16 with q
+        off[q] = (int32_t)(x * ld + pos * 16);
+        r_of_chunk = pos * 16;
+      } else {
+        static_assert(X >= 128, "the swizzle below is that of rows of 128 bytes and more");
+        const int r = c / (X / 16), pos = (c % (X / 16)) ^ (r & 7);
+        off[q] = (int32_t)(r * ld + pos * 16);
+      }
+    }
+  }
+  // Block b, of whose reduction `valid` indexes exist, to the tile at lds.
+  __device__ __forceinline__ void load(uint8_t* lds, int b, int valid) const {
+    const i32x4 from = buffer(base + b * step, left - b * step);
+    const bool none = kContig && r_of_chunk >= valid;
+    const uint32_t to = lds_address(lds) + uniform((int)threadIdx.x / 64) * 1024;
+#pragma unroll
+    for (int q = 0; q < T::kChunks; q++) load_to_lds_16(from, to + q * kThreads * 16, none ? kPastEnd : off[q]);
+  }
+};
+
+// This lane's LDS offsets of the fragments of rows x, x + 16, ... of a tile, x a multiple of 16 (kContig) or 64.
+template <bool kContig, int X, int N>
+struct Reader {
+  int at[kContig ? 2 : N];
+  __device__ __forceinline__ explicit Reader(int x) {
+    const int lane = threadIdx.x & 63, g = lane / 16, i = lane % 16;
+    using T = Tile<kContig, X, 64>;
+    if constexpr (kContig) {
+      at[0] = T::at(i, 2 * g) + x * kR;
+      at[1] = T::at(i, 2 * g + 1) + x * kR;
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; n++) at[n] = T::at(32 * g + i / 2, x / 16 + n) + (i & 1) * 8;
+    }
+  }
+  __device__ __forceinline__ i32x8 fragment(const uint8_t* lds, int n) const {
+    i32x8 f;
+    if constexpr (kContig) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + at[0] + 16 * n * kR);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + at[1] + 16 * n * kR);
+      f = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; t++) {
+        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(MXQ_LDS(i32x2, lds + at[n] + 8 * t * X));
+        f[2 * t] = w[0];
+        f[2 * t + 1] = w[1];
+      }
+    }
+    return f;
+  }
+};
+
+// Codes of a tile's rows, one 32-bit word a row in LDS.  Where four blocks' codes
+// of a row are an aligned word in memory they come in one load every four blocks,
+// else byte by byte, every block.
+template <int X, int kThreads>
+struct CodeFeed {
+  const uint8_t* base;
+  int64_t step, left;
+  int32_t off;
+  bool words;
+  static constexpr int kWaves = X / 64;
+
+  __device__ __forceinline__ CodeFeed(const uint8_t* code, const Operand& o, int x0, int x_end, int blocks, int first_wave) {
+    const int64_t start = (int64_t)(x0 >> o.x_shift) * o.code_x;
+    base = uniform(code + start);
+    step = o.code_r;
+    left = uniform((int64_t)((x_end - 1) >> o.x_shift) * o.code_x + (blocks - 1) * step + 1 - start);
+    words = step == 1 && blocks % 4 == 0 && o.code_x % 4 == 0 && ((uintptr_t)base & 3) == 0;
+    const int x = min(x0 + ((int)threadIdx.x - first_wave * 64), x_end - 1);
+    off = (int32_t)(((x >> o.x_shift) - (x0 >> o.x_shift)) * o.code_x);
+  }
+  // Called by the kWaves waves from first_wave on.
+  __device__ __forceinline__ void load(uint32_t* lds, int b, int first_wave) const {
+    const i32x4 from = buffer(base + b * step, left - b * step);
+    const uint32_t to = lds_address(place(lds, b)) + (uniform((int)threadIdx.x / 64) - first_wave) * 256;
+    if (!words) load_to_lds_1(from, to, off);
+    else if (b % 4 == 0) load_to_lds_4(from, to, off);
+  }
+  // Where block b's words are, and by how many bits they are shifted.
+  __device__ __forceinline__ const uint32_t* place(const uint32_t* lds, int b) const {
+    return lds + (words ? b / 4 & 1 : b & 1) * X;
+  }
+  __device__ __forceinline__ int shift(int b) const { return words ? 8 * (b & 3) : 0; }
+};
+
+template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void tile_kernel(Args a, int ti, int tj) {
+  constexpr int kWaves = BI / WI * (BJ / WJ), kThreads = kWaves * 64;
+  constexpr bool kVContig = kMode != kWgrad, kUContig = kMode == kForward;
+  using TV = Tile<kVContig, BI, kThreads>;
+  using TU = Tile<kUContig, BJ, kThreads>;
+  constexpr int kStage = TV::kBytes + TU::kBytes;
+  static_assert(BI / 64 + BJ / 64 == kWaves, "one load of codes a wave");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint32_t codes_v[2 * BI], codes_u[2 * BJ];
+
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x / 64);
+  const int wi = wave / (BJ / WJ) * WI, wj = wave % (BJ / WJ) * WJ;
+  const int bi = blockIdx.x / tj, bj = blockIdx.x % tj;
+  const int j0 = bj * BJ;
+  int i0 = bi * BI, i_end = a.I, r_begin = 0, r_end = a.R, expert = 0;
+  int64_t code_block = 0;
+  if (a.offsets) {
+    if constexpr (kMode == kWgrad) {
+      expert = blockIdx.z;
+      const Segment s = mxq_dev::find_expert<kR>(a.offsets, a.experts, a.R, expert);
+      r_begin = uniform(s.lo), r_end = uniform(s.hi), code_block = uniform(s.first);
+    } else {
+      const Segment s = mxq_dev::find_tile<BI>(a.offsets, a.experts, a.I, bi);
+      expert = uniform(s.expert);
+      i0 = uniform((int)min((int64_t)s.lo + (int64_t)s.tile * BI, (int64_t)s.hi)), i_end = uniform(s.hi);
+      if (i0 >= i_end) return;
+      if (expert == a.experts) r_end = r_begin;
+    }
+  }
+  const int ue = kMode == kWgrad || expert == a.experts ? 0 : expert;
+  const int blocks = (r_end - r_begin + kR - 1) / kR;
+
+  f32x4 acc[WJ / 16][WI / 16];
+#pragma unroll
+  for (int j = 0; j < WJ / 16; j++)
+#pragma unroll
+    for (int i = 0; i < WI / 16; i++) acc[j][i] = f32x4{0, 0, 0, 0};
+
+  const Feed<kVContig, BI, kThreads> v(a.v.data, a.v.ld, i0, i_end, r_begin, r_end);
+  const Feed<kUContig, BJ, kThreads> u(a.u.data + ue * a.u.expert_stride, a.u.ld, j0, a.J, r_begin, r_end);
+  const CodeFeed<BI, kThreads> vc(a.v.code + code_block * a.v.code_r, a.v, i0, i_end, blocks, 0);
+  const CodeFeed<BJ, kThreads> uc(a.u.code + ue * a.u.code_expert_stride + code_block * a.u.code_r, a.u, j0, a.J, blocks,
+                                  BI / 64);
+  const Reader<kVContig, BI, WI / 16> rv(wi);
+  const Reader<kUContig, BJ, WJ / 16> ru(wj);
+  auto load = [&](int b) {
+    uint8_t* const to = lds + (b & 1) * kStage;
+    if (wave < BI / 64) vc.load(codes_v, b, 0);
+    else uc.load(codes_u, b, BI / 64);
+    v.load(to, b, r_end - r_begin - b * kR);
+    u.load(to + TV::kBytes, b, r_end - r_begin - b * kR);
+  };
+  if (blocks) load(0);
+  for (int b = 0; b < blocks; b++) {
+    arrive();   // block b is in LDS, and no wave reads block b - 1 any more
+    if (b + 1 < blocks) load(b + 1);
+    const uint8_t* const lv = lds + (b & 1) * kStage;
+    const uint8_t* const lu = lv + TV::kBytes;
+    const uint32_t* const wv = vc.place(codes_v, b) + wi;
+    const uint32_t* const wu = uc.place(codes_u, b) + wj;
+    i32x8 fv[WI / 16];
+    int cv[WI / 16];
+#pragma unroll
+    for (int i = 0; i < WI / 16; i++) {
+      cv[i] = wv[16 * i + lane % 16] >> vc.shift(b) & 255;
+      fv[i] = rv.fragment(lv, i);
+    }
+    const Prepared<kFast, WI / 16> pv(fv);
+#pragma unroll
+    for (int j = 0; j < WJ / 16; j++) {
+      Codes<kFast> cu;
+#pragma unroll
+      for (int t = 0; t < (kFast ? 1 : 4); t++)
+        cu.c[t] = wu[16 * j + (kFast ? lane % 16 : lane / 16 * 4 + t)] >> uc.shift(b) & 255;
+      multiply<kFast>(acc[j], pv, cv, ru.fragment(lu, j), cu);
+    }
+  }
+
+  TO* const out = reinterpret_cast<TO*>(a.out) + (kMode == kWgrad ? expert * a.out_expert_stride : 0);
+#pragma unroll
+  for (int i = 0; i < WI / 16; i++) {
+    const int row = i0 + wi + 16 * i + lane % 16;
+    if (row >= i_end) continue;
+#pragma unroll
+    for (int j = 0; j < WJ / 16; j++) {
+      const int col = j0 + wj + 16 * j + lane / 16 * 4;
+      if (col < a.J) store4(out + row * a.ld_out + col, acc[j][i], a.J - col, a.vec_out);
+    }
+  }
+}
+
+template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
+int launch_tiles(const Args& a, hipStream_t stream) {
+  const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
+  int64_t ti = ((int64_t)a.I + BI - 1) / BI, tz = 1;
+  if (a.offsets) {
+    if (kMode == kWgrad) tz = a.experts;
+    else ti = a.I / BI + a.experts + 2;
+  }
+  if (ti * tj > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
+  hipLaunchKernelGGL((tile_kernel<kMode, kFast, TO, BI, BJ, WI, WJ>), dim3((uint32_t)(ti * tj), 1, (uint32_t)tz),
+                     dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)ti, (int)tj);
+  return launch_status();
+}
+
+// Whether an operand's tiles can be fed straight to LDS: 16-byte aligned rows,
+// whole chunks along the contiguous axis, 32-bit offsets within a tile.
+bool feedable(const Operand& o, int contiguous, int64_t experts) {
+  return aligned(o.data, 16) && o.ld % 16 == 0 && contiguous % 16 == 0 && o.ld < ((int64_t)1 << 22) &&
+         o.code_x < ((int64_t)1 << 22) && (experts <= 1 || o.expert_stride % 16 == 0);
+}
+
 // ---- few rows -------------------------------------------------------------------------------
 // With few rows i a product is bound by reading U once, so nothing is shared
 // between waves on the way: each of a workgroup's waves takes every kWaves-th
@@ -485,6 +756,10 @@ int launch(const Args& a, hipStream_t stream) {
     if (rows <= 16) return launch_few<kMode, kFast, TO, 1, kMode == kDgrad ? 8 : 4>(a, stream);
     if (rows <= 32) return launch_few<kMode, kFast, TO, 2, 4>(a, stream);
     if (rows <= 64) return launch_few<kMode, kFast, TO, 4, 4>(a, stream);
+  }
+  if (feedable(a.v, kMode == kWgrad ? a.I : a.R, 0) && feedable(a.u, kMode == kForward ? a.R : a.J, a.experts)) {
+    if constexpr (kFast) return launch_tiles<kMode, kFast, TO, 256, 256, 128, 64>(a, stream);
+    else return launch_tiles<kMode, kFast, TO, 128, 128, 64, 64>(a, stream);
   }
   constexpr int BI = 128, BJ = 128, WI = 64, WJ = 64;
   const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
