@@ -706,6 +706,35 @@ def mxq_quantize_mxfp4_grouped(xs, packeds=None, scales=None, scale_ld: Optional
 
 # ---- FP8 products and the routing of a layer of experts ------------------------------------
 
+# A call on a single token costs more on the host than on the GPU, so these
+# functions take the short way where there is one.
+
+_UINT8, _INT32, _FLOAT32 = torch.uint8, torch.int32, torch.float32
+_FLOAT_CODES = {torch.bfloat16: MXQ_BF16, torch.float32: MXQ_FP32}
+
+
+def _library(name: str) -> ctypes.CDLL:
+    return _libs.get(name) or load(name)
+
+
+def _mat(t: torch.Tensor):
+    """_matrix, at once for the usual contiguous [rows, K]."""
+    s = t.shape
+    if len(s) == 2 and t.is_contiguous():
+        return t.data_ptr(), s[0], s[1], s[1]
+    return _matrix(t)
+
+
+def _handle(t: torch.Tensor):
+    """torch's current stream on t's device as the C calls take it."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _float_code(t: torch.Tensor) -> int:
+    code = _FLOAT_CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
 def _ng(n: int) -> int:
     return (n + 127) // 128
 
@@ -734,17 +763,17 @@ def _code_rows(rows: int, n_experts: int) -> int:
 
 def _source(x: torch.Tensor, slots: Optional[torch.Tensor], top_k: int):
     """The quantizer's leading arguments, and the rows and columns of its result."""
-    px, x_rows, K, ldx = _matrix(x)
+    px, x_rows, K, ldx = _mat(x)
     if slots is None:
-        return (px, ldx, x_rows, x_rows, K, _dtype_code(x), None, 1), x_rows, K
+        return (px, ldx, x_rows, x_rows, K, _float_code(x), None, 1), x_rows, K
     rows = slots.numel()
-    return (px, ldx, x_rows, rows, K, _dtype_code(x), _vector(slots, rows, torch.int32, "slots"), top_k), rows, K
+    return (px, ldx, x_rows, rows, K, _float_code(x), _vector(slots, rows, torch.int32, "slots"), top_k), rows, K
 
 
 def _bytes_for(x: torch.Tensor, t: Optional[torch.Tensor], rows: int, cols: int, what: str):
     """(tensor, pointer, row stride) of a byte output, allocated if missing."""
     if t is None:
-        t = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        t = torch.empty((rows, cols), dtype=_UINT8, device=x.device)
         return t, t.data_ptr(), cols
     p, ld = _operand(t, rows, cols, what, byte=True)
     return t, p, ld
@@ -758,11 +787,11 @@ def mxq_quantize_fp8_group128(x: torch.Tensor, slots: Optional[torch.Tensor] = N
     (payload uint8 [rows, K], codes uint8 [rows, ceil(K/128)]).  With `slots` (int32, as
     mxq_sort_experts returns them) row r of the result is x's row slots[r] // top_k, zeros for a
     dropped slot."""
-    L = load(lib)
+    L = _library(lib)
     args, rows, K = _source(x, slots, top_k)
     data, pd, ldd = _bytes_for(x, data, rows, K, "payload")
     scale, ps, lds = _bytes_for(x, scale, rows, _ng(K), "scale")
-    _check(L, L.mxq_quantize_fp8_group128(*args, pd, ldd, ps, lds, _stream(x)))
+    _check(L, L.mxq_quantize_fp8_group128(*args, pd, ldd, ps, lds, _handle(x)))
     return data, scale
 
 
@@ -773,12 +802,12 @@ def mxq_quantize_fp8_group128_col(x: torch.Tensor, slots: Optional[torch.Tensor]
     """The same with groups of 128 rows of a column, the operand of a weight gradient ->
     (payload uint8 [rows, K], codes uint8 [groups, K]).  With `offsets` (int32 [n_experts + 1])
     groups begin anew with each expert's rows and there are rows // 128 + n_experts code rows."""
-    L = load(lib)
+    L = _library(lib)
     args, rows, K = _source(x, slots, top_k)
     po, n = _experts_of(offsets)
     data, pd, ldd = _bytes_for(x, data, rows, K, "payload")
     scale, ps, lds = _bytes_for(x, scale, _code_rows(rows, n), K, "scale")
-    _check(L, L.mxq_quantize_fp8_group128_col(*args, po, n, pd, ldd, ps, lds, _stream(x)))
+    _check(L, L.mxq_quantize_fp8_group128_col(*args, po, n, pd, ldd, ps, lds, _handle(x)))
     return data, scale
 
 
@@ -790,20 +819,26 @@ def mxq_quantize_fp8_group128_row_col(x: torch.Tensor, slots: Optional[torch.Ten
                                       lib: str = "libmxq.so"):
     """Groups along the rows and along the columns from one read of x ->
     (row payload, row codes, column payload, column codes)."""
-    L = load(lib)
+    L = _library(lib)
     args, rows, K = _source(x, slots, top_k)
     po, n = _experts_of(offsets)
     row_data, prd, ldrd = _bytes_for(x, row_data, rows, K, "row payload")
     row_scale, prs, ldrs = _bytes_for(x, row_scale, rows, _ng(K), "row_scale")
     col_data, pcd, ldcd = _bytes_for(x, col_data, rows, K, "column payload")
     col_scale, pcs, ldcs = _bytes_for(x, col_scale, _code_rows(rows, n), K, "col_scale")
-    _check(L, L.mxq_quantize_fp8_group128_row_col(*args, po, n, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs, _stream(x)))
+    _check(L, L.mxq_quantize_fp8_group128_row_col(*args, po, n, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs, _handle(x)))
     return row_data, row_scale, col_data, col_scale
 
 
 def _weights(w: torch.Tensor, tile_code: torch.Tensor, n_experts: int):
     """(N, K, the C call's arguments) of [N, K] payloads and their tile codes, n_experts of them if not 0."""
     lead = 3 if n_experts else 2
+    ws, ts = w.shape, tile_code.shape
+    if (len(ws) == len(ts) == lead and w.is_contiguous() and tile_code.is_contiguous() and w.element_size() == 1
+            and tile_code.element_size() == 1 and ts[-2:] == (_ng(ws[-2]), _ng(ws[-1]))
+            and (not n_experts or ws[0] == ts[0] == n_experts)):
+        N, K, tc = ws[-2], ws[-1], ts[-1]
+        return N, K, (w.data_ptr(), K, N * K, tile_code.data_ptr(), tc, ts[-2] * tc)
     if w.dim() != lead or tile_code.dim() != lead or (n_experts and not w.shape[0] == tile_code.shape[0] == n_experts):
         raise ValueError("w and tile_code are [N, K] and [ceil(N/128), ceil(K/128)], with offsets [n_experts, ...] "
                          f"of them; got {list(w.shape)} and {list(tile_code.shape)}")
@@ -821,10 +856,13 @@ def _weights(w: torch.Tensor, tile_code: torch.Tensor, n_experts: int):
 
 def _rows_operand(t: torch.Tensor, scale: torch.Tensor, cols: int, what: str):
     """(rows, the C call's arguments) of a payload [rows, cols] with row groups."""
-    p, rows, tcols, ld = _matrix(t)
+    p, rows, tcols, ld = _mat(t)
     if tcols != cols or t.element_size() != 1:
         raise ValueError(f"{what} holds bytes, [rows, {cols}], got {t.dtype} {list(t.shape)}")
-    ps, lds = _operand(scale, rows, _ng(cols), what + "_scale", byte=True)
+    groups = _ng(cols)
+    if scale.shape == (rows, groups) and scale.is_contiguous() and scale.element_size() == 1:
+        return rows, (p, ld, scale.data_ptr(), groups)
+    ps, lds = _operand(scale, rows, groups, what + "_scale", byte=True)
     return rows, (p, ld, ps, lds)
 
 
@@ -832,11 +870,12 @@ def _result(like: torch.Tensor, out: Optional[torch.Tensor], shape, out_dtype: t
     """(tensor, pointer, row stride, stride of a leading dimension, dtype) of an output, allocated if missing."""
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=like.device)
-    elif tuple(out.shape) != tuple(shape):
+        return out, out.data_ptr(), shape[-1], shape[-2] * shape[-1], _float_code(out)
+    if tuple(out.shape) != tuple(shape):
         raise ValueError(f"the output is {list(shape)}, got {list(out.shape)}")
     if shape[-1] > 1 and out.stride(-1) != 1:
         raise ValueError("the last dimension must be contiguous")
-    return out, out.data_ptr(), out.stride(-2) if shape[-2] > 1 else shape[-1], out.stride(0), _dtype_code(out)
+    return out, out.data_ptr(), out.stride(-2) if shape[-2] > 1 else shape[-1], out.stride(0), _float_code(out)
 
 
 @_device_operands
@@ -849,12 +888,12 @@ def mxq_matmul_fp8_block128(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Ten
     [n_experts + 1]) the rows of x are sorted by expert, w is [n_experts, N, K] and expert e's rows
     meet w[e]; rows of no expert give zeros.  Products are summed in fp32; with `fast_accum` the FP8
     matrix instructions sum them, at about twice the rate and up to 2^-10 of the sum of magnitudes off."""
-    L = load(lib)
-    po, n = _experts_of(offsets)
+    L = _library(lib)
+    po, n = (None, 0) if offsets is None else _experts_of(offsets)
     N, K, pw = _weights(w, tile_code, n)
     M, px = _rows_operand(x, x_scale, K, "x")
     out, py, ldy, _, dt = _result(x, out, (M, N), out_dtype)
-    _check(L, L.mxq_matmul_fp8_block128(*px, *pw, M, N, K, po, n, py, ldy, dt, fast_accum, _stream(x)))
+    _check(L, L.mxq_matmul_fp8_block128(*px, *pw, M, N, K, po, n, py, ldy, dt, fast_accum, _handle(x)))
     return out
 
 
@@ -865,12 +904,12 @@ def mxq_matmul_fp8_block128_dgrad(dy: torch.Tensor, dy_scale: torch.Tensor, w: t
                                   lib: str = "libmxq.so") -> torch.Tensor:
     """dx = dy w in FP8, the input's gradient of mxq_matmul_fp8_block128: dy [M, N] with its codes
     [M, ceil(N/128)], the same w and tile codes -> [M, K]."""
-    L = load(lib)
-    po, n = _experts_of(offsets)
+    L = _library(lib)
+    po, n = (None, 0) if offsets is None else _experts_of(offsets)
     N, K, pw = _weights(w, tile_code, n)
     M, pg = _rows_operand(dy, dy_scale, N, "dy")
     out, px, ldx, _, dt = _result(dy, out, (M, K), out_dtype)
-    _check(L, L.mxq_matmul_fp8_block128_dgrad(*pg, *pw, M, N, K, po, n, px, ldx, dt, fast_accum, _stream(dy)))
+    _check(L, L.mxq_matmul_fp8_block128_dgrad(*pg, *pw, M, N, K, po, n, px, ldx, dt, fast_accum, _handle(dy)))
     return out
 
 
@@ -880,10 +919,10 @@ def mxq_matmul_fp8_group128_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: t
                                   out_dtype: torch.dtype = torch.float32, lib: str = "libmxq.so") -> torch.Tensor:
     """dw = dy^T x in FP8, the weight's gradient: dy [M, N] and x [M, K] with the codes of column groups
     (mxq_quantize_fp8_group128_col, both with the same `offsets`) -> [N, K], or [n_experts, N, K]."""
-    L = load(lib)
+    L = _library(lib)
     po, n = _experts_of(offsets)
-    pg, M, N, ldg = _matrix(dy)
-    px, mx, K, ldx = _matrix(x)
+    pg, M, N, ldg = _mat(dy)
+    px, mx, K, ldx = _mat(x)
     if mx != M or dy.element_size() != 1 or x.element_size() != 1:
         raise ValueError(f"dy and x hold bytes and have the same rows, got {dy.dtype} {list(dy.shape)} and "
                          f"{x.dtype} {list(x.shape)}")
@@ -892,7 +931,7 @@ def mxq_matmul_fp8_group128_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: t
     pxs, ldxs = _operand(x_scale, groups, K, "x_scale", byte=True)
     out, pw, ldw, stride, dt = _result(dy, out, (n, N, K) if n else (N, K), out_dtype)
     _check(L, L.mxq_matmul_fp8_group128_wgrad(pg, ldg, pgs, ldgs, px, ldx, pxs, ldxs, M, N, K, po, n, pw, ldw, stride,
-                                              dt, _stream(dy)))
+                                              dt, _handle(dy)))
     return out
 
 
@@ -903,19 +942,20 @@ def mxq_sort_experts(ids: torch.Tensor, n_experts: int, lib: str = "libmxq.so"):
     owns sorted rows offsets[e] .. offsets[e + 1]; slots[r] is the slot of sorted row r and
     position[t, j] the sorted row of slot t * top_k + j.  Ids outside [0, n_experts) are dropped:
     their slots come last and both directions hold the complement."""
-    L = load(lib)
+    L = _library(lib)
     if ids.dim() != 2 or ids.dtype != torch.int32:
         raise ValueError(f"ids is int32 [tokens, top_k], got {ids.dtype} {list(ids.shape)}")
-    pi, T, k, ldi = _matrix(ids)
+    pi, T, k, ldi = _mat(ids)
     need = L.mxq_sort_experts_workspace(T, k, n_experts)
     # one allocation: offsets, slots, position, workspace
     n = T * k
-    buf = torch.empty(n_experts + 1 + 2 * n + need // 4, dtype=torch.int32, device=ids.device)
+    a = n_experts + 1
+    buf = torch.empty(a + 2 * n + need // 4, dtype=_INT32, device=ids.device)
     at = buf.data_ptr()
-    a, b = n_experts + 1, n_experts + 1 + n
-    _check(L, L.mxq_sort_experts(pi, ldi, T, k, n_experts, at, at + 4 * a, at + 4 * b, at + 4 * (b + n), need,
-                                 _stream(ids)))
-    return buf[:a], buf[a:b], buf[b:b + n].view(T, k)
+    _check(L, L.mxq_sort_experts(pi, ldi, T, k, n_experts, at, at + 4 * a, at + 4 * (a + n), at + 4 * (a + 2 * n), need,
+                                 _handle(ids)))
+    offsets, slots, position = (buf[:a + 2 * n] if need else buf).split_with_sizes((a, n, n))
+    return offsets, slots, position.view(T, k)
 
 
 @_device_operands
@@ -923,14 +963,14 @@ def mxq_dispatch_rows(x: torch.Tensor, slots: torch.Tensor, top_k: int, out: Opt
                       lib: str = "libmxq.so") -> torch.Tensor:
     """x's rows (bf16 / fp32 [tokens, H]) in sorted order: row r is x[slots[r] // top_k], zeros for a
     dropped slot -> [slots, H].  Its gradient is mxq_combine_rows without weights."""
-    L = load(lib)
-    px, T, H, ldx = _matrix(x)
+    L = _library(lib)
+    px, T, H, ldx = _mat(x)
     rows = slots.numel()
     ps = _vector(slots, rows, torch.int32, "slots")
     out, po, ldo, _, dt = _result(x, out, (rows, H), x.dtype)
     if out.dtype != x.dtype:
         raise ValueError("out must have x's dtype")
-    _check(L, L.mxq_dispatch_rows(px, ldx, T, ps, rows, top_k, H, dt, po, ldo, _stream(x)))
+    _check(L, L.mxq_dispatch_rows(px, ldx, T, ps, rows, top_k, H, dt, po, ldo, _handle(x)))
     return out
 
 
@@ -947,13 +987,13 @@ def mxq_combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Option
                      out: Optional[torch.Tensor] = None, lib: str = "libmxq.so") -> torch.Tensor:
     """Sorted rows (bf16 / fp32 [rows, H]) back to their tokens: y[t] = sum over j of weights[t, j] *
     rows[position[t, j]] -> [tokens, H].  `weights` fp32 [tokens, top_k], None: all 1."""
-    L = load(lib)
-    pr, R, H, ldr = _matrix(rows)
+    L = _library(lib)
+    pr, R, H, ldr = _mat(rows)
     T, k, pp, pw = _slots_of(position, weights)
     out, py, ldy, _, dt = _result(rows, out, (T, H), rows.dtype)
     if out.dtype != rows.dtype:
         raise ValueError("out must have the rows' dtype")
-    _check(L, L.mxq_combine_rows(pr, ldr, R, pp, pw, T, k, H, dt, py, ldy, _stream(rows)))
+    _check(L, L.mxq_combine_rows(pr, ldr, R, pp, pw, T, k, H, dt, py, ldy, _handle(rows)))
     return out
 
 
@@ -963,9 +1003,9 @@ def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: to
                               dweights: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
     """Gradients of mxq_combine_rows for dy [tokens, H] -> (drows [rows, H], dweights fp32 [tokens, top_k]).
     `position` names every row once, as mxq_sort_experts returns it."""
-    L = load(lib)
-    pg, T0, H, ldg = _matrix(dy)
-    pr, R, hr, ldr = _matrix(rows)
+    L = _library(lib)
+    pg, T0, H, ldg = _mat(dy)
+    pr, R, hr, ldr = _mat(rows)
     T, k, pp, pw = _slots_of(position, weights)
     if (T0, hr) != (T, H) or dy.dtype != rows.dtype:
         raise ValueError(f"dy is [tokens, H] of the rows' dtype, got {dy.dtype} {list(dy.shape)} for "
@@ -976,7 +1016,7 @@ def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: to
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     pv = _vector(dweights, T * k, torch.float32, "dweights")
-    _check(L, L.mxq_combine_rows_backward(pg, ldg, pr, ldr, R, pp, pw, T, k, H, dt, pd, ldd, pv, _stream(dy)))
+    _check(L, L.mxq_combine_rows_backward(pg, ldg, pr, ldr, R, pp, pw, T, k, H, dt, pd, ldd, pv, _handle(dy)))
     return drows, dweights
 
 

@@ -85,11 +85,17 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* p, int avail) {
   return v;
 }
 
-// A tile of X rows (of V or U) by kR of the reduction in LDS, in 16-byte chunks.
-// kContig: [X][kR], chunk c of row x at place c ^ (x / 2 % 8): the 16 rows that a
-// wave's lanes read at once then fall on all 64 banks.  Else [kR][X], chunk c of
-// row r at place c ^ (r % 8) (rows of 64 bytes: c ^ (r / 4 % 4)), for the same
-// reason: 16 lanes read one chunk of 8 consecutive rows.
+// Which reduction indexes of a block a lane holds: chunks g and g + 4 of 16, g =
+// lane / 16.  V and U agree on it, and it is all that the products ask for.
+__device__ __forceinline__ int chunk_of(int g, int half) { return g + 4 * half; }
+
+// A tile of X rows (of V or U) by kR of the reduction in LDS, in 16-byte chunks,
+// each row's chunks in an order of its own so that what lanes read at once falls
+// on different banks of the 64 (no bank conflict is counted):
+// kContig: [X][kR], chunk c of row x at place c ^ (x / 2 % 8).  A read takes one
+// chunk of 16 rows in each of the four lane groups.
+// Else [kR][X], chunk c of row r at place c ^ turn(r).  A read takes one chunk of
+// 8 rows in each lane group, whose rows are 16 apart.
 template <bool kContig, int X, int kThreads>
 struct Tile {
   static constexpr int kChunks = X * kR / 16 / kThreads;
@@ -97,9 +103,13 @@ struct Tile {
 
   // LDS offset of chunk pos of row x (kContig) or r.
   static __device__ __forceinline__ int at(int row, int pos) {
-    if constexpr (kContig) return row * kR + ((pos ^ ((row >> 1) & 7)) << 4);
-    else if constexpr (X == 64) return row * X + ((pos ^ ((row >> 2) & 3)) << 4);
-    else return row * X + ((pos ^ (row & 7)) << 4);
+    return row * (kContig ? kR : X) + ((pos ^ turn(row)) << 4);
+  }
+  static __device__ __forceinline__ int turn(int row) {
+    if constexpr (kContig) return (row >> 1) & 7;
+    else if constexpr (X == 64) return ((row >> 2) & 1) | ((row >> 3) & 2);
+    else if constexpr (X == 128) return (row & 6) | ((row >> 4) & 1);
+    else return (row & 7) | ((row >> 1) & 8);
   }
   static __device__ __forceinline__ int place(int q) {
     const int c = threadIdx.x + q * kThreads;
@@ -118,18 +128,18 @@ struct Tile {
       return load16(base + r * ld + x, r < r_end ? x_end - x : 0);
     }
   }
-  // Operand registers of rows x .. x + 15: lane l holds row x + l % 16, reduction 32 (l / 16) .. + 31.
+  // Operand registers of rows x .. x + 15: lane l holds row x + l % 16.
   static __device__ __forceinline__ i32x8 fragment(const uint8_t* lds, int x) {
     const int lane = threadIdx.x & 63, g = lane / 16, i = lane % 16;
     i32x8 f;
     if constexpr (kContig) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + at(x + i, 2 * g));
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + at(x + i, 2 * g + 1));
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + at(x + i, chunk_of(g, 0)));
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + at(x + i, chunk_of(g, 1)));
       f = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
-        const int r = 32 * g + 8 * t + i / 2;
+        const int r = 16 * chunk_of(g, t / 2) + t % 2 * 8 + i / 2;
         const uint8_t* p = lds + at(r, x >> 4) + (i & 1) * 8;
         const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(MXQ_LDS(i32x2, p));
         f[2 * t] = w[0];
@@ -390,12 +400,11 @@ struct Feed {
     for (int q = 0; q < T::kChunks; q++) {
       const int c = threadIdx.x + q * kThreads;
       if constexpr (kContig) {
-        const int x = c / 8, pos = (c % 8) ^ ((x >> 1) & 7);   // x advances by multiples of 16 with q
+        const int x = c / 8, pos = (c % 8) ^ T::turn(x);   // x advances by multiples of 16 with q
         off[q] = (int32_t)(x * ld + pos * 16);
         r_of_chunk = pos * 16;
       } else {
-        static_assert(X >= 128, "the swizzle below is that of rows of 128 bytes and more");
-        const int r = c / (X / 16), pos = (c % (X / 16)) ^ (r & 7);
+        const int r = c / (X / 16), pos = (c % (X / 16)) ^ T::turn(r);
         off[q] = (int32_t)(r * ld + pos * 16);
       }
     }
@@ -418,11 +427,11 @@ struct Reader {
     const int lane = threadIdx.x & 63, g = lane / 16, i = lane % 16;
     using T = Tile<kContig, X, 64>;
     if constexpr (kContig) {
-      at[0] = T::at(i, 2 * g) + x * kR;
-      at[1] = T::at(i, 2 * g + 1) + x * kR;
+      at[0] = T::at(i, chunk_of(g, 0)) + x * kR;
+      at[1] = T::at(i, chunk_of(g, 1)) + x * kR;
     } else {
 #pragma unroll
-      for (int n = 0; n < N; n++) at[n] = T::at(32 * g + i / 2, x / 16 + n) + (i & 1) * 8;
+      for (int n = 0; n < N; n++) at[n] = T::at(16 * chunk_of(g, 0) + i / 2, x / 16 + n) + (i & 1) * 8;
     }
   }
   __device__ __forceinline__ i32x8 fragment(const uint8_t* lds, int n) const {
@@ -434,7 +443,7 @@ struct Reader {
     } else {
 #pragma unroll
       for (int t = 0; t < 4; t++) {
-        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(MXQ_LDS(i32x2, lds + at[n] + 8 * t * X));
+        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(MXQ_LDS(i32x2, lds + at[n] + (t / 2 * 64 + t % 2 * 8) * X));
         f[2 * t] = w[0];
         f[2 * t + 1] = w[1];
       }
@@ -599,9 +608,10 @@ bool feedable(const Operand& o, int contiguous, int64_t experts) {
 // (dx), a wave turns its block around in an LDS tile of its own.
 constexpr int kFewWaves = 8;
 
-// Reduction r .. r + 31 of a row, of which the first r_end - r are the operand's.
+// This lane's part of reduction r .. r + 127 of a row, which ends at r_end.
 __device__ __forceinline__ i32x8 row_fragment(const uint8_t* row, int r, int r_end) {
-  const i32x4 lo = load16(row + r, r_end - r), hi = load16(row + r + 16, r_end - r - 16);
+  const int g = (threadIdx.x & 63) / 16, r0 = r + 16 * chunk_of(g, 0), r1 = r + 16 * chunk_of(g, 1);
+  const i32x4 lo = load16(row + r0, r_end - r0), hi = load16(row + r1, r_end - r1);
   return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
@@ -655,7 +665,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
     i32x4 raw[kTurn ? kChunks : 1];
   };
   auto load = [&](Block& k, int b) {
-    const int r = b * kR + lane / 16 * 32;
+    const int r = b * kR;
     if constexpr (kTurn) {
 #pragma unroll
       for (int q = 0; q < kChunks; q++) {
