@@ -45,11 +45,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x4_u __attribute__((ext_vector_type(4), aligned(1)));   // a 16-byte load at any address
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4_w __attribute__((ext_vector_type(4), aligned(4)));   // 16 bytes at a word's address
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+#define MXQ_LDS_AT(T, a) ((__attribute__((address_space(3))) T*)(uint32_t)(a))
 #define MXQ_LDS(T, p) ((__attribute__((address_space(3))) T*)(p))
 
 constexpr int kR = 128;   // the reduction block: one group, one product instruction
@@ -75,15 +77,69 @@ struct Args {
   bool vec_out;
 };
 
-// 16 bytes at p of which the first `avail` are the operand's; the others are 0.
-__device__ __forceinline__ i32x4 load16(const uint8_t* p, int avail) {
-  if (avail >= 16) return *reinterpret_cast<const i32x4_u*>(p);
-  i32x4 v{0, 0, 0, 0};
+// 16 bytes on their way from p, of which the first `avail` are wanted and the
+// others are 0.  The memory pipeline is slow at addresses that are no multiple of 4
+// (odd row strides took 4 times as long), so such bytes come as the aligned words
+// around them and are shifted into place by done(), when they are needed.  Every
+// word that is read holds at least one wanted byte.
+__device__ __forceinline__ i32x4 first_bytes(i32x4 w, int n) {
 #pragma unroll
-  for (int i = 0; i < 16; i++)
-    if (i < avail) v[i / 4] |= (int)((uint32_t)p[i] << (8 * (i & 3)));
-  return v;
+  for (int k = 0; k < 4; k++) {
+    const int m = n - 4 * k;
+    w[k] &= m >= 4 ? -1 : m > 0 ? (1 << (8 * m)) - 1 : 0;
+  }
+  return w;
 }
+template <bool kAligned>
+struct Bytes16;
+template <>
+struct Bytes16<true> {   // p is a multiple of 16
+  i32x4 w;
+  __device__ __forceinline__ Bytes16() {}
+  __device__ __forceinline__ Bytes16(const uint8_t* p, int avail) {
+    if (avail >= 16) {
+      w = *reinterpret_cast<const i32x4*>(p);
+      return;
+    }
+    const int last = (avail - 1) / 4;
+    i32x4 v{0, 0, 0, 0};
+    if (avail > 0) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) v[k] = reinterpret_cast<const int*>(p)[min(k, last)];
+    }
+    w = first_bytes(v, avail);
+  }
+  __device__ __forceinline__ i32x4 done() const { return w; }
+};
+template <>
+struct Bytes16<false> {
+  i32x4 w;
+  int more, shift, wanted;
+  __device__ __forceinline__ Bytes16() {}
+  __device__ __forceinline__ Bytes16(const uint8_t* p, int avail) {
+    shift = (int)((uintptr_t)p & 3);
+    wanted = avail;
+    const int* const q = reinterpret_cast<const int*>(p - shift);
+    if (avail >= 16) {
+      w = *reinterpret_cast<const i32x4_w*>(q);
+      more = q[shift ? 4 : 3];
+      return;
+    }
+    w = i32x4{0, 0, 0, 0};
+    more = 0;
+    if (avail > 0) {
+      const int last = (shift + avail - 1) / 4;
+#pragma unroll
+      for (int k = 0; k < 4; k++) w[k] = q[min(k, last)];
+      more = q[last];
+    }
+  }
+  __device__ __forceinline__ i32x4 done() const {
+    const i32x4 v{(int)__builtin_amdgcn_alignbyte(w[1], w[0], shift), (int)__builtin_amdgcn_alignbyte(w[2], w[1], shift),
+                  (int)__builtin_amdgcn_alignbyte(w[3], w[2], shift), (int)__builtin_amdgcn_alignbyte(more, w[3], shift)};
+    return __all(wanted >= 16) ? v : first_bytes(v, wanted);
+  }
+};
 
 // Which reduction indexes of a block a lane holds: chunks g and g + 4 of 16, g =
 // lane / 16.  V and U agree on it, and it is all that the products ask for.
@@ -96,9 +152,8 @@ __device__ __forceinline__ int chunk_of(int g, int half) { return g + 4 * half; 
 // chunk of 16 rows in each of the four lane groups.
 // Else [kR][X], chunk c of row r at place c ^ turn(r).  A read takes one chunk of
 // 8 rows in each lane group, whose rows are 16 apart.
-template <bool kContig, int X, int kThreads>
+template <bool kContig, int X>
 struct Tile {
-  static constexpr int kChunks = X * kR / 16 / kThreads;
   static constexpr int kBytes = X * kR;
 
   // LDS offset of chunk pos of row x (kContig) or r.
@@ -110,23 +165,6 @@ struct Tile {
     else if constexpr (X == 64) return ((row >> 2) & 1) | ((row >> 3) & 2);
     else if constexpr (X == 128) return (row & 6) | ((row >> 4) & 1);
     else return (row & 7) | ((row >> 1) & 8);
-  }
-  static __device__ __forceinline__ int place(int q) {
-    const int c = threadIdx.x + q * kThreads;
-    if constexpr (kContig) return at(c / 8, c % 8);
-    else return at(c / (X / 16), c % (X / 16));
-  }
-  // Chunk q of this thread: rows x0 .. of at most x_end, reduction r0 .. of at most r_end.
-  static __device__ __forceinline__ i32x4 load(const uint8_t* base, int64_t ld, int x0, int x_end, int r0, int r_end,
-                                               int q) {
-    const int c = threadIdx.x + q * kThreads;
-    if constexpr (kContig) {
-      const int x = x0 + c / 8, r = r0 + c % 8 * 16;
-      return load16(base + x * ld + r, x < x_end ? r_end - r : 0);
-    } else {
-      const int r = r0 + c / (X / 16), x = x0 + c % (X / 16) * 16;
-      return load16(base + r * ld + x, r < r_end ? x_end - x : 0);
-    }
   }
   // Operand registers of rows x .. x + 15: lane l holds row x + l % 16.
   static __device__ __forceinline__ i32x8 fragment(const uint8_t* lds, int x) {
@@ -214,18 +252,6 @@ template <bool kFast>
 struct Codes {
   int c[kFast ? 1 : 4];
 };
-template <bool kFast>
-__device__ __forceinline__ Codes<kFast> u_codes(const Args& a, const uint8_t* uc, int col, int64_t b) {
-  const int lane = threadIdx.x & 63;
-  Codes<kFast> k;
-#pragma unroll
-  for (int t = 0; t < (kFast ? 1 : 4); t++) {
-    const int j = col + (kFast ? lane % 16 : lane / 16 * 4 + t);
-    k.c[t] = j < a.J ? uc[(j >> a.u.x_shift) * a.u.code_x + b * a.u.code_r] : 127;
-  }
-  return k;
-}
-
 // One reduction block of 16 rows of U times 16 N rows of V, added to acc.
 template <bool kFast, int N>
 __device__ __forceinline__ void multiply(f32x4 (&acc)[N], const Prepared<kFast, N>& v, const int (&cv)[N], i32x8 u,
@@ -250,39 +276,104 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[N], const Prepared<kFast, 
   }
 }
 
-template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args a) {
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  return (const T*)uniform((int64_t)p);
+}
+
+// Which tile and segment a workgroup has.
+struct Work {
+  int i0, i_end, j0, r_begin, r_end, expert, weight;   // weight: the expert whose weight to read (0 where none is)
+  int64_t code_block;                                  // first reduction block's place among the codes
+  bool none;
+};
+template <Mode kMode, int BI, int BJ>
+__device__ __forceinline__ Work work_of(const Args& a, int bi, int bj) {
+  Work w{bi * BI, a.I, bj * BJ, 0, a.R, 0, 0, 0, false};
+  if (a.offsets) {
+    if constexpr (kMode == kWgrad) {
+      w.expert = blockIdx.z;
+      const Segment s = mxq_dev::find_expert<kR>(a.offsets, a.experts, a.R, w.expert);
+      w.r_begin = uniform(s.lo), w.r_end = uniform(s.hi), w.code_block = uniform(s.first);
+    } else {
+      const Segment s = mxq_dev::find_tile<BI>(a.offsets, a.experts, a.I, bi);
+      w.expert = uniform(s.expert);
+      w.i0 = uniform((int)min((int64_t)s.lo + (int64_t)s.tile * BI, (int64_t)s.hi)), w.i_end = uniform(s.hi);
+      w.none = w.i0 >= w.i_end;
+      if (w.expert == a.experts) w.r_end = w.r_begin;   // rows of no expert: zeros
+    }
+  }
+  w.weight = kMode == kWgrad || w.expert == a.experts ? 0 : w.expert;
+  return w;
+}
+
+// A wave's WI x WJ results, rows i and columns j on, of 16 x 16 products.
+template <typename TO, int WI, int WJ>
+__device__ __forceinline__ void store_tile(const Args& a, const Work& w, int i0, int j0, const f32x4 (&acc)[WJ / 16][WI / 16]) {
+  const int lane = threadIdx.x & 63;
+  TO* const out = reinterpret_cast<TO*>(a.out);
+#pragma unroll
+  for (int i = 0; i < WI / 16; i++) {
+    const int row = i0 + 16 * i + lane % 16;
+    if (row >= w.i_end) continue;
+#pragma unroll
+    for (int j = 0; j < WJ / 16; j++) {
+      const int col = j0 + 16 * j + lane / 16 * 4;
+      if (col < a.J) store4(out + row * a.ld_out + col, acc[j][i], a.J - col, a.vec_out);
+    }
+  }
+}
+
+// A tile of X rows by kR of the reduction on its way to LDS through registers,
+// for rows of any alignment; P says where its chunks go.
+template <typename P, bool kContig, int X, int kThreads>
+struct Carry {
+  static constexpr int kChunks = X * kR / 16 / kThreads, kPer = kContig ? kR / 16 : X / 16;
+  Bytes16<false> c[kChunks];
+  // rows x0 .. of at most x_end, reduction r0 .. of at most r_end
+  __device__ __forceinline__ void fetch(const uint8_t* base, int64_t ld, int x0, int x_end, int r0, int r_end) {
+#pragma unroll
+    for (int q = 0; q < kChunks; q++) {
+      const int at = threadIdx.x + q * kThreads;
+      if constexpr (kContig) {
+        const int x = min(x0 + at / kPer, x_end - 1), r = r0 + at % kPer * 16;   // what rows past the end add is not stored
+        c[q] = Bytes16<false>(base + x * ld + r, r_end - r);
+      } else {
+        const int r = r0 + at / kPer, x = x0 + at % kPer * 16;
+        c[q] = Bytes16<false>(base + r * ld + x, r < r_end ? x_end - x : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* lds) const {
+#pragma unroll
+    for (int q = 0; q < kChunks; q++) {
+      const int at = threadIdx.x + q * kThreads;
+      *reinterpret_cast<i32x4*>(lds + P::at(at / kPer, at % kPer)) = c[q].done();
+    }
+  }
+};
+
+template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void carried_kernel(Args a) {
   constexpr int kThreads = BI / WI * (BJ / WJ) * 64;
-  constexpr bool kVContig = kMode != kWgrad, kUContig = kMode == kForward;
-  using TV = Tile<kVContig, BI, kThreads>;
-  using TU = Tile<kUContig, BJ, kThreads>;
+  constexpr bool kUContig = kMode == kForward;
+  using TV = Tile<true, BI>;
+  using TU = Tile<kUContig, BJ>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TV::kBytes + TU::kBytes];
   uint8_t* const lv = lds;
   uint8_t* const lu = lds + TV::kBytes;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
   const int wi = wave / (BJ / WJ) * WI, wj = wave % (BJ / WJ) * WJ;
-  const int j0 = blockIdx.x * BJ;
-  int i0 = blockIdx.y * BI, i_end = a.I, r_begin = 0, r_end = a.R, expert = 0;
-  int64_t code_block = 0;   // first reduction block's place among the codes
-  if (a.offsets) {
-    if constexpr (kMode == kWgrad) {
-      expert = blockIdx.z;
-      const Segment s = mxq_dev::find_expert<kR>(a.offsets, a.experts, a.R, expert);
-      r_begin = s.lo, r_end = s.hi, code_block = s.first;
-    } else {
-      const Segment s = mxq_dev::find_tile<BI>(a.offsets, a.experts, a.I, blockIdx.y);
-      expert = s.expert;
-      i0 = min((int64_t)s.lo + (int64_t)s.tile * BI, (int64_t)s.hi), i_end = s.hi;
-      if (i0 >= i_end) return;
-      if (expert == a.experts) r_end = r_begin;   // rows of no expert: zeros
-    }
-  }
-  const int ue = kMode == kWgrad ? 0 : (expert == a.experts ? 0 : expert);
-  const uint8_t* const vd = a.v.data;
-  const uint8_t* const ud = a.u.data + ue * a.u.expert_stride;
-  const uint8_t* const vc = a.v.code + code_block * a.v.code_r;
-  const uint8_t* const uc = a.u.code + ue * a.u.code_expert_stride + code_block * a.u.code_r;
+  const Work w = work_of<kMode, BI, BJ>(a, blockIdx.y, blockIdx.x);
+  if (w.none) return;
+  const uint8_t* const ud = a.u.data + w.weight * a.u.expert_stride;
+  const uint8_t* const uc = a.u.code + w.weight * a.u.code_expert_stride;
 
   f32x4 acc[WJ / 16][WI / 16];
 #pragma unroll
@@ -290,43 +381,45 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args 
 #pragma unroll
     for (int i = 0; i < WI / 16; i++) acc[j][i] = f32x4{0, 0, 0, 0};
 
-  for (int r0 = r_begin, b = 0; r0 < r_end; r0 += kR, b++) {
-    i32x4 sv[TV::kChunks], su[TU::kChunks];
-#pragma unroll
-    for (int q = 0; q < TV::kChunks; q++) sv[q] = TV::load(vd, a.v.ld, i0, i_end, r0, r_end, q);
-#pragma unroll
-    for (int q = 0; q < TU::kChunks; q++) su[q] = TU::load(ud, a.u.ld, j0, a.J, r0, r_end, q);
+  Carry<TV, true, BI, kThreads> sv;   // a block ahead of the products
+  Carry<TU, kUContig, BJ, kThreads> su;
+  auto fetch = [&](int r0) {
+    sv.fetch(a.v.data, a.v.ld, w.i0, w.i_end, r0, w.r_end);
+    su.fetch(ud, a.u.ld, w.j0, a.J, r0, w.r_end);
+  };
+  if (w.r_end) fetch(0);
+  for (int b = 0; b * kR < w.r_end; b++) {
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < TV::kChunks; q++) *reinterpret_cast<i32x4*>(lv + TV::place(q)) = sv[q];
-#pragma unroll
-    for (int q = 0; q < TU::kChunks; q++) *reinterpret_cast<i32x4*>(lu + TU::place(q)) = su[q];
+    sv.store(lv);
+    su.store(lu);
     __syncthreads();
+    if ((b + 1) * kR < w.r_end) fetch((b + 1) * kR);
     int cv[WI / 16];
     i32x8 fv[WI / 16];
 #pragma unroll
     for (int i = 0; i < WI / 16; i++) {
-      const int row = i0 + wi + 16 * i + lane % 16;
-      cv[i] = row < i_end ? vc[row * a.v.code_x + b * a.v.code_r] : 127;
+      const int row = min(w.i0 + wi + 16 * i + lane % 16, w.i_end - 1);
+      cv[i] = a.v.code[row * a.v.code_x + b * a.v.code_r];
       fv[i] = TV::fragment(lv, wi + 16 * i);
     }
-    const Prepared<kFast, WI / 16> pv(fv);
-#pragma unroll
-    for (int j = 0; j < WJ / 16; j++)
-      multiply<kFast>(acc[j], pv, cv, TU::fragment(lu, wj + 16 * j), u_codes<kFast>(a, uc, j0 + wj + 16 * j, b));
-  }
-
-  TO* const out = reinterpret_cast<TO*>(a.out) + (kMode == kWgrad ? expert * a.out_expert_stride : 0);
-#pragma unroll
-  for (int i = 0; i < WI / 16; i++) {
-    const int row = i0 + wi + 16 * i + lane % 16;
-    if (row >= i_end) continue;
+    const Prepared<true, WI / 16> pv(fv);
 #pragma unroll
     for (int j = 0; j < WJ / 16; j++) {
-      const int col = j0 + wj + 16 * j + lane / 16 * 4;
-      if (col < a.J) store4(out + row * a.ld_out + col, acc[j][i], a.J - col, a.vec_out);
+      const int col = min(w.j0 + wj + 16 * j, a.J - 1);   // 16 neighbouring columns lie in one tile
+      const Codes<true> cu{{uc[(col >> 7) * a.u.code_x + b * a.u.code_r]}};
+      multiply<true>(acc[j], pv, cv, TU::fragment(lu, wj + 16 * j), cu);
     }
   }
+  store_tile<TO, WI, WJ>(a, w, w.i0 + wi, w.j0 + wj, acc);
+}
+
+template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
+int launch_carried(const Args& a, hipStream_t stream) {
+  const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ, ti = a.offsets ? a.I / BI + a.experts + 2 : ((int64_t)a.I + BI - 1) / BI;
+  if (ti > 65535) return MXQ_ERR_SHAPE;
+  hipLaunchKernelGGL((carried_kernel<kMode, TO, BI, BJ, WI, WJ>), dim3((uint32_t)tj, (uint32_t)ti),
+                     dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a);
+  return launch_status();
 }
 
 // ---- many rows ------------------------------------------------------------------------------
@@ -338,16 +431,6 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void product_kernel(Args 
 //
 // Needs 16-byte aligned rows (and a contiguous axis that ends on a whole chunk).
 
-
-// A value that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
-}
-template <typename T>
-__device__ __forceinline__ const T* uniform(const T* p) {
-  return (const T*)uniform((int64_t)p);
-}
 
 // Loads from a buffer to LDS.  A buffer is bytes [base, base + left), at most
 // 2^31 - 1 of them; offsets at or past its end read zeros.  A wave's lanes write
@@ -372,15 +455,20 @@ MXQ_LOAD_TO_LDS(load_to_lds_16, "buffer_load_dwordx4")
 MXQ_LOAD_TO_LDS(load_to_lds_4, "buffer_load_dword")
 MXQ_LOAD_TO_LDS(load_to_lds_1, "buffer_load_ubyte")
 #undef MXQ_LOAD_TO_LDS
+// Waits for this wave's loads to LDS but the last kLeft, then for the workgroup.
+template <int kLeft>
+__device__ __forceinline__ void arrive_but() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
 __device__ __forceinline__ void arrive() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <bool kContig, int X, int kThreads>
+template <typename P, bool kContig, int X, int kThreads>
 struct Feed {
-  using T = Tile<kContig, X, kThreads>;
+  static constexpr int kChunks = X * kR / 16 / kThreads;
   const uint8_t* base;   // row x0, block 0
   int64_t step;          // bytes from one block to the next
   int64_t left;          // bytes from base to the operand's end
-  int32_t off[T::kChunks];
+  int32_t off[kChunks];
   int32_t r_of_chunk;    // kContig: reduction index within the block, the same for all of this lane's chunks
 
   // rows x0 .. x_end - 1 (of the axis that the output keeps), reduction r0 .. r_end - 1
@@ -397,14 +485,14 @@ struct Feed {
     left = uniform(left);
     r_of_chunk = 0;
 #pragma unroll
-    for (int q = 0; q < T::kChunks; q++) {
+    for (int q = 0; q < kChunks; q++) {
       const int c = threadIdx.x + q * kThreads;
       if constexpr (kContig) {
-        const int x = c / 8, pos = (c % 8) ^ T::turn(x);   // x advances by multiples of 16 with q
+        const int x = c / 8, pos = (c % 8) ^ P::turn(x);   // x advances by multiples of 16 with q
         off[q] = (int32_t)(x * ld + pos * 16);
         r_of_chunk = pos * 16;
       } else {
-        const int r = c / (X / 16), pos = (c % (X / 16)) ^ T::turn(r);
+        const int r = c / (X / 16), pos = (c % (X / 16)) ^ P::turn(r);
         off[q] = (int32_t)(r * ld + pos * 16);
       }
     }
@@ -415,7 +503,7 @@ struct Feed {
     const bool none = kContig && r_of_chunk >= valid;
     const uint32_t to = lds_address(lds) + uniform((int)threadIdx.x / 64) * 1024;
 #pragma unroll
-    for (int q = 0; q < T::kChunks; q++) load_to_lds_16(from, to + q * kThreads * 16, none ? kPastEnd : off[q]);
+    for (int q = 0; q < kChunks; q++) load_to_lds_16(from, to + q * kThreads * 16, none ? kPastEnd : off[q]);
   }
 };
 
@@ -425,7 +513,7 @@ struct Reader {
   int at[kContig ? 2 : N];
   __device__ __forceinline__ explicit Reader(int x) {
     const int lane = threadIdx.x & 63, g = lane / 16, i = lane % 16;
-    using T = Tile<kContig, X, 64>;
+    using T = Tile<kContig, X>;
     if constexpr (kContig) {
       at[0] = T::at(i, chunk_of(g, 0)) + x * kR;
       at[1] = T::at(i, chunk_of(g, 1)) + x * kR;
@@ -486,12 +574,12 @@ struct CodeFeed {
   __device__ __forceinline__ int shift(int b) const { return words ? 8 * (b & 3) : 0; }
 };
 
-template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
+template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
 __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void tile_kernel(Args a, int ti, int tj) {
   constexpr int kWaves = BI / WI * (BJ / WJ), kThreads = kWaves * 64;
-  constexpr bool kVContig = kMode != kWgrad, kUContig = kMode == kForward;
-  using TV = Tile<kVContig, BI, kThreads>;
-  using TU = Tile<kUContig, BJ, kThreads>;
+  constexpr bool kUContig = kMode == kForward;
+  using TV = Tile<true, BI>;
+  using TU = Tile<kUContig, BJ>;
   constexpr int kStage = TV::kBytes + TU::kBytes;
   static_assert(BI / 64 + BJ / 64 == kWaves, "one load of codes a wave");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
@@ -499,25 +587,9 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void tile_kernel(Args a, 
 
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x / 64);
   const int wi = wave / (BJ / WJ) * WI, wj = wave % (BJ / WJ) * WJ;
-  const int bi = blockIdx.x / tj, bj = blockIdx.x % tj;
-  const int j0 = bj * BJ;
-  int i0 = bi * BI, i_end = a.I, r_begin = 0, r_end = a.R, expert = 0;
-  int64_t code_block = 0;
-  if (a.offsets) {
-    if constexpr (kMode == kWgrad) {
-      expert = blockIdx.z;
-      const Segment s = mxq_dev::find_expert<kR>(a.offsets, a.experts, a.R, expert);
-      r_begin = uniform(s.lo), r_end = uniform(s.hi), code_block = uniform(s.first);
-    } else {
-      const Segment s = mxq_dev::find_tile<BI>(a.offsets, a.experts, a.I, bi);
-      expert = uniform(s.expert);
-      i0 = uniform((int)min((int64_t)s.lo + (int64_t)s.tile * BI, (int64_t)s.hi)), i_end = uniform(s.hi);
-      if (i0 >= i_end) return;
-      if (expert == a.experts) r_end = r_begin;
-    }
-  }
-  const int ue = kMode == kWgrad || expert == a.experts ? 0 : expert;
-  const int blocks = (r_end - r_begin + kR - 1) / kR;
+  const Work w = work_of<kMode, BI, BJ>(a, blockIdx.x / tj, blockIdx.x % tj);
+  if (w.none) return;
+  const int blocks = (w.r_end + kR - 1) / kR;
 
   f32x4 acc[WJ / 16][WI / 16];
 #pragma unroll
@@ -525,19 +597,18 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void tile_kernel(Args a, 
 #pragma unroll
     for (int i = 0; i < WI / 16; i++) acc[j][i] = f32x4{0, 0, 0, 0};
 
-  const Feed<kVContig, BI, kThreads> v(a.v.data, a.v.ld, i0, i_end, r_begin, r_end);
-  const Feed<kUContig, BJ, kThreads> u(a.u.data + ue * a.u.expert_stride, a.u.ld, j0, a.J, r_begin, r_end);
-  const CodeFeed<BI, kThreads> vc(a.v.code + code_block * a.v.code_r, a.v, i0, i_end, blocks, 0);
-  const CodeFeed<BJ, kThreads> uc(a.u.code + ue * a.u.code_expert_stride + code_block * a.u.code_r, a.u, j0, a.J, blocks,
-                                  BI / 64);
-  const Reader<kVContig, BI, WI / 16> rv(wi);
+  const Feed<TV, true, BI, kThreads> v(a.v.data, a.v.ld, w.i0, w.i_end, 0, w.r_end);
+  const Feed<TU, kUContig, BJ, kThreads> u(a.u.data + w.weight * a.u.expert_stride, a.u.ld, w.j0, a.J, 0, w.r_end);
+  const CodeFeed<BI, kThreads> vc(a.v.code, a.v, w.i0, w.i_end, blocks, 0);
+  const CodeFeed<BJ, kThreads> uc(a.u.code + w.weight * a.u.code_expert_stride, a.u, w.j0, a.J, blocks, BI / 64);
+  const Reader<true, BI, WI / 16> rv(wi);
   const Reader<kUContig, BJ, WJ / 16> ru(wj);
   auto load = [&](int b) {
     uint8_t* const to = lds + (b & 1) * kStage;
     if (wave < BI / 64) vc.load(codes_v, b, 0);
     else uc.load(codes_u, b, BI / 64);
-    v.load(to, b, r_end - r_begin - b * kR);
-    u.load(to + TV::kBytes, b, r_end - r_begin - b * kR);
+    v.load(to, b, w.r_end - b * kR);
+    u.load(to + TV::kBytes, b, w.r_end - b * kR);
   };
   if (blocks) load(0);
   for (int b = 0; b < blocks; b++) {
@@ -554,32 +625,307 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void tile_kernel(Args a, 
       cv[i] = wv[16 * i + lane % 16] >> vc.shift(b) & 255;
       fv[i] = rv.fragment(lv, i);
     }
-    const Prepared<kFast, WI / 16> pv(fv);
+    const Prepared<true, WI / 16> pv(fv);
 #pragma unroll
     for (int j = 0; j < WJ / 16; j++) {
-      Codes<kFast> cu;
-#pragma unroll
-      for (int t = 0; t < (kFast ? 1 : 4); t++)
-        cu.c[t] = wu[16 * j + (kFast ? lane % 16 : lane / 16 * 4 + t)] >> uc.shift(b) & 255;
-      multiply<kFast>(acc[j], pv, cv, ru.fragment(lu, j), cu);
+      Codes<true> cu;
+      cu.c[0] = wu[16 * j + lane % 16] >> uc.shift(b) & 255;
+      multiply<true>(acc[j], pv, cv, ru.fragment(lu, j), cu);
     }
   }
 
-  TO* const out = reinterpret_cast<TO*>(a.out) + (kMode == kWgrad ? expert * a.out_expert_stride : 0);
+  store_tile<TO, WI, WJ>(a, w, w.i0 + wi, w.j0 + wj, acc);
+}
+
+template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
+int launch_tiles(const Args& a, hipStream_t stream) {
+  const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
+  const int64_t ti = a.offsets ? a.I / BI + a.experts + 2 : ((int64_t)a.I + BI - 1) / BI;
+  if (ti * tj > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
+  hipLaunchKernelGGL((tile_kernel<kMode, TO, BI, BJ, WI, WJ>), dim3((uint32_t)(ti * tj)),
+                     dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)ti, (int)tj);
+  return launch_status();
+}
+
+// ---- many rows, sums in fp32 ------------------------------------------------------------------
+// Places of a tile's 16-byte chunks in LDS for fragments of 32 rows and 64
+// reduction indexes: a lane holds row lane % 32 and, with p = lane / 32, chunks
+// p, p + 2 (first half of the block) and p + 4, p + 6 (second half).
+// kContig: [X][kR], chunk c of row x at place c ^ (x / 2 % 8).  Else [kR][X], chunk
+// c of row r at place c ^ turn(r): the transposing read takes two neighbouring
+// chunks of 8 rows at once, which then fall on all 64 banks.
+template <bool kContig, int X>
+struct Places {
+  static __device__ __forceinline__ int turn(int row) {
+    if constexpr (kContig) return (row >> 1) & 7;
+    else if constexpr (X == 128) return row & 6;
+    else return (row & 7) << 1;
+  }
+  static __device__ __forceinline__ int at(int row, int c) { return row * (kContig ? kR : X) + ((c ^ turn(row)) << 4); }
+};
+
+// The codes of 64 of a tile's rows, one 32-bit word each in LDS; each wave brings
+// those of other rows, of V or of U.
+struct ByteCodeFeed {
+  const uint8_t* base;
+  int64_t step, left;
+  int32_t off;
+
+  // codes of rows x0 .. x_end - 1, lane by lane, `blocks` blocks from `code` on
+  __device__ __forceinline__ ByteCodeFeed(const uint8_t* code, int64_t code_x, int64_t code_r, int shift, int x0, int x_end,
+                                      int blocks) {
+    const int64_t first = min(x0, x_end - 1) >> shift;
+    base = uniform(code + first * code_x);
+    step = code_r;
+    left = uniform((((x_end - 1) >> shift) - first) * code_x + (blocks - 1) * code_r + 1);
+    off = (int32_t)(((min(x0 + ((int)threadIdx.x & 63), x_end - 1) >> shift) - first) * code_x);
+  }
+  __device__ __forceinline__ void load(uint32_t to, int b) const {
+    load_to_lds_1(buffer(base + b * step, left - b * step), to, off);
+  }
+};
+
+// 32 rows' payloads of one block: two halves of 64 reduction indexes.
+struct Rows32 {
+  i32x8 h[2];
+};
+
+// This lane's LDS addresses of the fragments of rows x, x + 32, ... of a tile, x a multiple of 32.
+template <bool kContig, int X, int N>
+struct Reader32 {
+  static constexpr int kCount = kContig ? 4 : N;
+  uint32_t at[kCount];
+  __device__ __forceinline__ Reader32(const uint8_t* tile, int x) {
+    const int lane = threadIdx.x & 63, p = lane / 32;
+    using P = Places<kContig, X>;
+    const uint32_t base = lds_address(tile);
+    if constexpr (kContig) {
 #pragma unroll
-  for (int i = 0; i < WI / 16; i++) {
-    const int row = i0 + wi + 16 * i + lane % 16;
-    if (row >= i_end) continue;
+      for (int q = 0; q < 4; q++) at[q] = base + P::at(lane % 32, p + 2 * q) + x * kR;
+    } else {
+      const int i = lane % 16;
 #pragma unroll
-    for (int j = 0; j < WJ / 16; j++) {
-      const int col = j0 + wj + 16 * j + lane / 16 * 4;
-      if (col < a.J) store4(out + row * a.ld_out + col, acc[j][i], a.J - col, a.vec_out);
+      for (int n = 0; n < N; n++) at[n] = base + P::at(16 * p + i / 2, x / 16 + 2 * n + lane / 16 % 2) + (i & 1) * 8;
     }
+  }
+  __device__ __forceinline__ Rows32 rows(uint32_t stage, int n) const {
+    Rows32 f;
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        if constexpr (kContig) {
+          const i32x4 w = *MXQ_LDS_AT(i32x4, at[2 * h + q] + stage + 32 * n * kR);
+#pragma unroll
+          for (int t = 0; t < 4; t++) f.h[h][4 * q + t] = w[t];
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                MXQ_LDS_AT(i32x2, at[n] + stage + (64 * h + 32 * q + 8 * t) * X));
+            f.h[h][4 * q + 2 * t] = w[0];
+            f.h[h][4 * q + 2 * t + 1] = w[1];
+          }
+        }
+      }
+    return f;
+  }
+  // Reads after this stay after it.
+  __device__ __forceinline__ void pin() {
+#pragma unroll
+    for (int n = 0; n < kCount; n++) asm volatile("" : "+v"(at[n]));
+  }
+};
+
+// 64 payloads of a row as bf16 times 2^(code - 127).
+struct Wide64 {
+  bf16x8 v[8];
+};
+__device__ __forceinline__ Wide64 widen(const Rows32& f, float scale) {
+  Wide64 w;
+#pragma unroll
+  for (int k = 0; k < 16; k++) {
+    const int word = f.h[k / 8][k % 8];
+    const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, scale, false);
+    const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, scale, true);
+    bf16x8& to = w.v[k / 2];
+    to[4 * (k % 2)] = lo[0], to[4 * (k % 2) + 1] = lo[1], to[4 * (k % 2) + 2] = hi[0], to[4 * (k % 2) + 3] = hi[1];
+  }
+  return w;
+}
+
+// Sums in fp32 take the codes into the conversion to bf16 where no value can leave
+// bf16's normal range by it and no product fp32's: codes from 77 to 246 (group
+// maxima from about 4e-13 to 3e38).  A block with any other code, 255 among them,
+// is summed unscaled, then scaled exactly.
+constexpr uint32_t kPlainFirst = 77, kPlainLast = 246;
+__device__ __forceinline__ bool plain_code(uint32_t code) { return code - kPlainFirst <= kPlainLast - kPlainFirst; }
+__device__ __forceinline__ float two_to(uint32_t code) { return __builtin_bit_cast(float, code << 23); }
+
+
+template <Mode kMode, bool kFed, typename TO, int BI, int BJ, int WI, int WJ, int kStages>
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void exact_kernel(Args a, int ti, int tj) {
+  constexpr int kWaves = BI / WI * (BJ / WJ), kThreads = kWaves * 64, NI = WI / 32, NJ = WJ / 32;
+  constexpr bool kVContig = kMode != kWgrad, kUContig = kMode == kForward;
+  constexpr int kVBytes = BI * kR, kStage = kVBytes + BJ * kR;
+  using FV = Feed<Places<kVContig, BI>, kVContig, BI, kThreads>;
+  using FU = Feed<Places<kUContig, BJ>, kUContig, BJ, kThreads>;
+  constexpr int kLoads = FV::kChunks + FU::kChunks + 1;   // a wave's loads to LDS of one block
+  static_assert(BI / 64 + BJ / 64 == kWaves, "64 rows' codes a wave");
+  static_assert(kLoads * (kStages - 2) < 64, "the count of loads that a wave can wait for");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[kStages * kStage];
+  __shared__ __attribute__((aligned(16))) uint32_t codes[kStages][BI + BJ];
+
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x / 64);
+  const int wi = wave / (BJ / WJ) * WI, wj = wave % (BJ / WJ) * WJ;
+  const Work w = work_of<kMode, BI, BJ>(a, blockIdx.x / tj, blockIdx.x % tj);
+  if (w.none) return;
+  const int blocks = (w.r_end - w.r_begin + kR - 1) / kR;
+
+  f32x16 acc[NJ][NI];
+#pragma unroll
+  for (int j = 0; j < NJ; j++)
+#pragma unroll
+    for (int i = 0; i < NI; i++) acc[j][i] = f32x16{};
+
+  const uint8_t* const ud = a.u.data + w.weight * a.u.expert_stride;
+  const FV v(a.v.data, a.v.ld, w.i0, w.i_end, w.r_begin, w.r_end);
+  const FU u(ud, a.u.ld, w.j0, a.J, w.r_begin, w.r_end);
+  Carry<Places<kVContig, BI>, kVContig, BI, kThreads> sv;   // unless kFed
+  Carry<Places<kUContig, BJ>, kUContig, BJ, kThreads> su;
+  auto fetch = [&](int b) {
+    sv.fetch(a.v.data, a.v.ld, w.i0, w.i_end, w.r_begin + b * kR, w.r_end);
+    su.fetch(ud, a.u.ld, w.j0, a.J, w.r_begin + b * kR, w.r_end);
+  };
+  const ByteCodeFeed c =
+      wave < BI / 64
+          ? ByteCodeFeed(a.v.code + w.code_block * a.v.code_r, a.v.code_x, a.v.code_r, a.v.x_shift, w.i0 + wave * 64,
+                         w.i_end, blocks)
+          : ByteCodeFeed(a.u.code + w.weight * a.u.code_expert_stride + w.code_block * a.u.code_r, a.u.code_x,
+                         a.u.code_r, a.u.x_shift, w.j0 + (wave - BI / 64) * 64, a.J, blocks);
+  const Reader32<kVContig, BI, NI> rv(lds, wi);
+  const Reader32<kUContig, BJ, NJ> ru(lds + kVBytes, wj);
+  auto load = [&](int b, int stage) {   // past the last block: zeros that nobody reads
+    uint8_t* const to = lds + stage * kStage;
+    c.load(lds_address(codes[stage]) + wave * 256, b);
+    v.load(to, b, w.r_end - w.r_begin - b * kR);
+    u.load(to + kVBytes, b, w.r_end - w.r_begin - b * kR);
+  };
+  if (blocks) {
+    if constexpr (kFed) {
+#pragma unroll
+      for (int s = 0; s < kStages - 1; s++) load(s, s);
+    } else {
+      fetch(0);
+    }
+  }
+  Rows32 fu[NJ];
+  uint32_t cu[NJ], cv[NI];
+  int b = 0, stage = 0;
+  auto begin = [&] {
+    if constexpr (kFed) {
+      arrive_but<kLoads * (kStages - 2)>();   // block b is in LDS, and no wave reads block b - 1 any more
+      load(b + kStages - 1, stage ? stage - 1 : kStages - 1);
+    } else {
+      // no wave reads block b - 2, whose place this is, since all came here for block b - 1
+      c.load(lds_address(codes[stage]) + wave * 256, b);
+      sv.store(lds + stage * kStage);
+      su.store(lds + stage * kStage + kVBytes);
+      arrive();
+      if (b + 1 < blocks) fetch(b + 1);
+    }
+  };
+  auto next = [&] {
+    b++;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  };
+  auto read = [&] {
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      cu[j] = codes[stage][BI + wj + 32 * j + lane % 32];
+      fu[j] = ru.rows(stage * kStage, j);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; i++) cv[i] = codes[stage][wi + 32 * i + lane % 32];
+  };
+  // Up to the first block with a code that is not plain, and from there on: two
+  // loops, so that the first one's registers know nothing of the other.
+  while (b < blocks) {
+    begin();
+    read();
+    bool plain = true;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) plain = plain && plain_code(cu[j]);
+#pragma unroll
+    for (int i = 0; i < NI; i++) plain = plain && plain_code(cv[i]);
+    if (!__all(plain)) break;
+    Wide64 wu[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; j++) wu[j] = widen(fu[j], two_to(cu[j]));
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+      const Wide64 wv = widen(rv.rows(stage * kStage, i), two_to(cv[i]));
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+#pragma unroll
+        for (int j = 0; j < NJ; j++)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wu[j].v[k], wv.v[k], acc[j][i], 0, 0, 0);
+    }
+    next();
+  }
+  bool begun = true;
+  while (b < blocks) {
+    if (!begun) {
+      begin();
+      read();
+    }
+    begun = false;
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+      const Wide64 wv = widen(rv.rows(stage * kStage, i), 1.0f);
+#pragma unroll
+      for (int j = 0; j < NJ; j++) {
+        const Wide64 wu = widen(fu[j], 1.0f);
+        f32x16 sum{};
+#pragma unroll
+        for (int k = 0; k < 8; k++) sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wu.v[k], wv.v[k], sum, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < 16; t++) {
+          const int code = __shfl((int)cu[j], t / 4 * 8 + lane / 32 * 4 + t % 4);
+          const float scaled = __builtin_ldexpf(sum[t], code + (int)cv[i] - 254);
+          acc[j][i][t] += code == 255 || cv[i] == 255 ? __builtin_nanf("") : scaled;
+        }
+      }
+    }
+    next();
+  }
+  // Results leave through LDS, a wave's own part of it, so that a store writes
+  // whole rows of WJ columns and not 32 bytes of each of 32 rows.
+  static_assert(WJ == 64 && kWaves * WI * WJ * 4 <= kStages * kStage, "a wave's results");
+  arrive();   // no wave reads LDS any more, and no load is on its way there
+  float* const own = reinterpret_cast<float*>(lds) + wave * WI * WJ;
+  auto place = [](int row, int chunk) { return row * WJ + ((chunk ^ (row & 15)) << 2); };
+#pragma unroll
+  for (int i = 0; i < NI; i++)
+#pragma unroll
+    for (int j = 0; j < NJ; j++)
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        *reinterpret_cast<f32x4*>(own + place(32 * i + lane % 32, 8 * j + 2 * q + lane / 32)) =
+            f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  TO* const out = reinterpret_cast<TO*>(a.out) + (kMode == kWgrad ? w.expert * a.out_expert_stride : 0);
+  const int col = w.j0 + wj + lane % 16 * 4;
+#pragma unroll 4
+  for (int r = lane / 16; r < WI; r += 4) {
+    const int row = w.i0 + wi + r;
+    const f32x4 y = *reinterpret_cast<const f32x4*>(own + place(r, lane % 16));
+    if (row < w.i_end && col < a.J) store4(out + row * a.ld_out + col, y, a.J - col, a.vec_out);
   }
 }
 
-template <Mode kMode, bool kFast, typename TO, int BI, int BJ, int WI, int WJ>
-int launch_tiles(const Args& a, hipStream_t stream) {
+template <Mode kMode, bool kFed, typename TO, int BI, int BJ, int WI, int WJ, int kStages>
+int launch_exact(const Args& a, hipStream_t stream) {
   const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
   int64_t ti = ((int64_t)a.I + BI - 1) / BI, tz = 1;
   if (a.offsets) {
@@ -587,16 +933,20 @@ int launch_tiles(const Args& a, hipStream_t stream) {
     else ti = a.I / BI + a.experts + 2;
   }
   if (ti * tj > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
-  hipLaunchKernelGGL((tile_kernel<kMode, kFast, TO, BI, BJ, WI, WJ>), dim3((uint32_t)(ti * tj), 1, (uint32_t)tz),
+  hipLaunchKernelGGL((exact_kernel<kMode, kFed, TO, BI, BJ, WI, WJ, kStages>), dim3((uint32_t)(ti * tj), 1, (uint32_t)tz),
                      dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)ti, (int)tj);
   return launch_status();
 }
 
-// Whether an operand's tiles can be fed straight to LDS: 16-byte aligned rows,
-// whole chunks along the contiguous axis, 32-bit offsets within a tile.
+// Whether all rows of an operand begin at multiples of 16 bytes.
+bool chunked(const Operand& o, int64_t experts) {
+  return aligned(o.data, 16) && o.ld % 16 == 0 && (experts <= 1 || o.expert_stride % 16 == 0);
+}
+
+// Whether an operand's tiles can be fed straight to LDS: rows at multiples of 16
+// bytes, whole chunks along the contiguous axis, 32-bit offsets within a tile.
 bool feedable(const Operand& o, int contiguous, int64_t experts) {
-  return aligned(o.data, 16) && o.ld % 16 == 0 && contiguous % 16 == 0 && o.ld < ((int64_t)1 << 22) &&
-         o.code_x < ((int64_t)1 << 22) && (experts <= 1 || o.expert_stride % 16 == 0);
+  return chunked(o, experts) && contiguous % 16 == 0 && o.ld < ((int64_t)1 << 22) && o.code_x < ((int64_t)1 << 22);
 }
 
 // ---- few rows -------------------------------------------------------------------------------
@@ -609,18 +959,30 @@ bool feedable(const Operand& o, int contiguous, int64_t experts) {
 constexpr int kFewWaves = 8;
 
 // This lane's part of reduction r .. r + 127 of a row, which ends at r_end.
-__device__ __forceinline__ i32x8 row_fragment(const uint8_t* row, int r, int r_end) {
-  const int g = (threadIdx.x & 63) / 16, r0 = r + 16 * chunk_of(g, 0), r1 = r + 16 * chunk_of(g, 1);
-  const i32x4 lo = load16(row + r0, r_end - r0), hi = load16(row + r1, r_end - r1);
-  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-}
+template <bool kAligned>
+struct RowPart {
+  Bytes16<kAligned> half[2];
+  __device__ __forceinline__ RowPart() {}
+  __device__ __forceinline__ RowPart(const uint8_t* row, int r, int r_end) {
+    const int g = (threadIdx.x & 63) / 16;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int at = r + 16 * chunk_of(g, h);
+      half[h] = Bytes16<kAligned>(row + at, r_end - at);
+    }
+  }
+  __device__ __forceinline__ i32x8 done() const {
+    const i32x4 lo = half[0].done(), hi = half[1].done();
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+};
 
-template <Mode kMode, bool kFast, typename TO, int kNI, int kNJ>
+template <Mode kMode, bool kFast, bool kAligned, typename TO, int kNI, int kNJ>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
   static_assert(kMode != kWgrad, "a weight gradient reduces over the rows");
   constexpr bool kTurn = kMode == kDgrad;
   constexpr int BJ = 16 * kNJ, kChunks = BJ * kR / 16 / 64;
-  using T = Tile<false, BJ, 64>;
+  using T = Tile<false, BJ>;
   constexpr int kSum = kNI * kNJ * 64 * 4;                       // floats of one wave's sums
   constexpr int kShared = kFewWaves / 2 * kSum * 4;
   constexpr int kTurned = kTurn ? kFewWaves * BJ * kR : 0;
@@ -659,10 +1021,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
   for (int j = 0; j < kNJ; j++) ucode[j] = uc + (min(j0 + 16 * j, a.J - 1) >> 7) * a.u.code_x;
 
   struct Block {
-    i32x8 v[kNI];
+    RowPart<kAligned> v[kNI];
     int cv[kNI], cu[kNJ];
-    i32x8 u[kTurn ? 1 : kNJ];
-    i32x4 raw[kTurn ? kChunks : 1];
+    RowPart<kAligned> u[kTurn ? 1 : kNJ];
+    Bytes16<kAligned> raw[kTurn ? kChunks : 1];
   };
   auto load = [&](Block& k, int b) {
     const int r = b * kR;
@@ -670,15 +1032,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
 #pragma unroll
       for (int q = 0; q < kChunks; q++) {
         const int c = lane + 64 * q, ur = b * kR + c / kNJ, uj = j0 + c % kNJ * 16;
-        k.raw[q] = load16(ud + ur * a.u.ld + uj, ur < a.R ? a.J - uj : 0);
+        k.raw[q] = Bytes16<kAligned>(ud + ur * a.u.ld + uj, ur < a.R ? a.J - uj : 0);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kNJ; j++) k.u[j] = row_fragment(urow[j], r, a.R);
+      for (int j = 0; j < kNJ; j++) k.u[j] = RowPart<kAligned>(urow[j], r, a.R);
     }
 #pragma unroll
     for (int i = 0; i < kNI; i++) {
-      k.v[i] = row_fragment(vrow[i], r, a.R);
+      k.v[i] = RowPart<kAligned>(vrow[i], r, a.R);
       k.cv[i] = vcode[i][b];
     }
 #pragma unroll
@@ -691,20 +1053,29 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < kNI; i++) acc[j][i] = f32x4{0, 0, 0, 0};
 
+  // Aligned blocks are loaded one ahead of the products; the words around
+  // unaligned ones take half as many registers again, which leaves no room for that.
   Block now, next;
-  if (wave < blocks) load(now, wave);
+  if (kAligned && wave < blocks) load(now, wave);
   for (int b = wave; b < blocks; b += kFewWaves) {
-    if (b + kFewWaves < blocks) load(next, b + kFewWaves);
+    if constexpr (kAligned) {
+      if (b + kFewWaves < blocks) load(next, b + kFewWaves);
+    } else {
+      load(now, b);
+    }
     if constexpr (kTurn) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int q = 0; q < kChunks; q++) {
         const int c = lane + 64 * q;
-        *reinterpret_cast<i32x4*>(tile + T::at(c / kNJ, c % kNJ)) = now.raw[q];
+        *reinterpret_cast<i32x4*>(tile + T::at(c / kNJ, c % kNJ)) = now.raw[q].done();
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    const Prepared<kFast, kNI> pv(now.v);
+    i32x8 fv[kNI];
+#pragma unroll
+    for (int i = 0; i < kNI; i++) fv[i] = now.v[i].done();
+    const Prepared<kFast, kNI> pv(fv);
 #pragma unroll
     for (int j = 0; j < kNJ; j++) {
       Codes<kFast> cu;   // 16 neighbouring columns lie in one tile
@@ -712,10 +1083,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(Args a) {
       for (int t = 0; t < (kFast ? 1 : 4); t++) cu.c[t] = now.cu[j];
       i32x8 u;
       if constexpr (kTurn) u = T::fragment(tile, 16 * j);
-      else u = now.u[j];
+      else u = now.u[j].done();
       multiply<kFast>(acc[j], pv, now.cv, u, cu);
     }
-    now = next;
+    if constexpr (kAligned) now = next;
   }
 
   float* const sums = reinterpret_cast<float*>(lds);
@@ -753,8 +1124,11 @@ int launch_few(const Args& a, hipStream_t stream) {
   const int64_t tj = ((int64_t)a.J + 16 * kNJ - 1) / (16 * kNJ);
   const int64_t ti = a.offsets ? a.I / (16 * kNI) + a.experts + 2 : ((int64_t)a.I + 16 * kNI - 1) / (16 * kNI);
   if (ti > 65535) return MXQ_ERR_SHAPE;
-  hipLaunchKernelGGL((few_rows_kernel<kMode, kFast, TO, kNI, kNJ>), dim3((uint32_t)tj, (uint32_t)ti),
-                     dim3(kFewWaves * 64), 0, stream, a);
+  const dim3 grid((uint32_t)tj, (uint32_t)ti), block(kFewWaves * 64);
+  if (chunked(a.v, 0) && chunked(a.u, a.experts))
+    hipLaunchKernelGGL((few_rows_kernel<kMode, kFast, true, TO, kNI, kNJ>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((few_rows_kernel<kMode, kFast, false, TO, kNI, kNJ>), grid, block, 0, stream, a);
   return launch_status();
 }
 
@@ -767,21 +1141,14 @@ int launch(const Args& a, hipStream_t stream) {
     if (rows <= 32) return launch_few<kMode, kFast, TO, 2, 4>(a, stream);
     if (rows <= 64) return launch_few<kMode, kFast, TO, 4, 4>(a, stream);
   }
-  if (feedable(a.v, kMode == kWgrad ? a.I : a.R, 0) && feedable(a.u, kMode == kForward ? a.R : a.J, a.experts)) {
-    if constexpr (kFast) return launch_tiles<kMode, kFast, TO, 256, 256, 128, 64>(a, stream);
-    else return launch_tiles<kMode, kFast, TO, 128, 128, 64, 64>(a, stream);
+  const bool fed = feedable(a.v, kMode == kWgrad ? a.I : a.R, 0) && feedable(a.u, kMode == kForward ? a.R : a.J, a.experts);
+  if constexpr (kFast) {
+    return fed ? launch_tiles<kMode, TO, 256, 256, 128, 64>(a, stream)
+               : launch_carried<kMode, TO, 128, 128, 64, 64>(a, stream);
+  } else {
+    return fed ? launch_exact<kMode, true, TO, 128, 128, 64, 64, 2>(a, stream)
+               : launch_exact<kMode, false, TO, 128, 128, 64, 64, 2>(a, stream);
   }
-  constexpr int BI = 128, BJ = 128, WI = 64, WJ = 64;
-  const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
-  int64_t ti = ((int64_t)a.I + BI - 1) / BI, tz = 1;
-  if (a.offsets) {
-    if (kMode == kWgrad) tz = a.experts;
-    else ti = a.I / BI + a.experts + 2;   // the experts' tiles and those of the rows of none
-  }
-  if (ti > 65535) return MXQ_ERR_SHAPE;
-  const dim3 grid((uint32_t)tj, (uint32_t)ti, (uint32_t)tz), block(BI / WI * (BJ / WJ) * 64);
-  hipLaunchKernelGGL((product_kernel<kMode, kFast, TO, BI, BJ, WI, WJ>), grid, block, 0, stream, a);
-  return launch_status();
 }
 
 // One operand as the caller gives it: a [rows, cols] payload and its codes.
