@@ -42,8 +42,8 @@ __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t ld, MxqDivi
 struct SortArgs {
   const int32_t* ids;
   int64_t ld;
-  MxqDivisor top_k;
-  int total, n, per_wave;   // slots in all, experts, slots per wave
+  MxqDivisor top_k, per_group;   // per_group: n + 1
+  int total, n, per_wave;        // slots in all, experts, slots per wave
   int32_t* offsets;
   int32_t* slots;
   int32_t* position;
@@ -79,7 +79,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* scratch) {
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
-  extern __shared__ int lds[];              // [waves][n + 1] counts, then next free places
+  extern __shared__ int lds[];              // [waves][n + 1] counts, then next free places; two more rows of sums
   __shared__ int scratch[kSortWaves];
   const int n1 = a.n + 1, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
   for (int i = threadIdx.x; i < kSortWaves * n1; i += kSortThreads) lds[i] = 0;
@@ -89,26 +89,40 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
   const int end = min(begin + a.per_wave, a.total);
   for (int s = begin + lane; s < end; s += 64) atomicAdd(&mine[expert_of(a.ids, a.ld, a.top_k, s, a.n)], 1);
   __syncthreads();
+  // the sums over all workgroups, and over those before this one, from the counts
+  // that the first launch left: all lanes at once, added up in LDS
+  int* const all = lds + kSortWaves * n1;
+  int* const before = all + n1;
+  if (a.counts) {
+    for (int e = threadIdx.x; e < 2 * n1; e += kSortThreads) all[e] = 0;
+    __syncthreads();
+    const int n = (int)gridDim.x * n1, mark = (int)blockIdx.x * n1;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += kSortThreads) {
+      const int c = a.counts[i], e = i - (int)mxq_quot((uint32_t)i, a.per_group) * n1;
+      if (c) {
+        atomicAdd(&all[e], c);
+        if (i < mark) atomicAdd(&before[e], c);
+      }
+    }
+    __syncthreads();
+  }
   // one expert a lane
   {
     static_assert(kMaxExperts < kSortThreads, "a lane for each expert and one for the dropped slots");
     const int e = threadIdx.x;
-    int all = 0, before = 0;
+    int total = 0;
     if (e < n1) {
       if (a.counts) {
-        for (int b = 0; b < (int)gridDim.x; b++) {
-          const int c = a.counts[(int64_t)b * n1 + e];
-          if (b < (int)blockIdx.x) before += c;
-          all += c;
-        }
+        total = all[e];
       } else {
-        for (int w = 0; w < kSortWaves; w++) all += lds[w * n1 + e];
+        for (int w = 0; w < kSortWaves; w++) total += lds[w * n1 + e];
       }
     }
-    const int start = block_exclusive(all, scratch);
+    const int start = block_exclusive(total, scratch);
     if (e < n1) {
       if (blockIdx.x == 0) a.offsets[e] = start;   // offsets[n]: where the dropped ones begin
-      int next = start + before;
+      int next = start + (a.counts ? before[e] : 0);
       for (int w = 0; w < kSortWaves; w++) {
         const int c = lds[w * n1 + e];
         lds[w * n1 + e] = next;
@@ -140,6 +154,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
     }
   }
 }
+
+// Results of more than this leave with the non-temporal hint: the L2s together
+// hold 32 MiB, and without it lines that nobody reads again push others out.
+// Sorting 131072 slots and bringing their rows of 2048 bf16
+// into order takes 183 us without and 156 with it; 8192 tokens of 6 such rows back
+// and their gradients 139 and 121.  Smaller results are left where the
+// next kernel finds them.
+constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 
 // ---- rows into sorted order and back ----------------------------------------------------------
 constexpr int kRowThreads = 256, kEPL = 8;
@@ -187,16 +209,20 @@ __device__ __forceinline__ typename Eight<T>::Raw load8(const T* row, int c, int
   }
   return v;
 }
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kStream = false>
 __device__ __forceinline__ void store8(T* row, int c, int H, typename Eight<T>::Raw v) {
   if (kVec) {
     if (c < H) {
       typedef u32x4 A __attribute__((may_alias));
+      auto put = [](T* p, u32x4 w) {
+        if constexpr (kStream) __builtin_nontemporal_store(w, reinterpret_cast<A*>(p));
+        else *reinterpret_cast<A*>(p) = w;
+      };
       if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<A*>(row + c) = v;
+        put(row + c, v);
       } else {
-        *reinterpret_cast<A*>(row + c) = __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 0, 1, 2, 3));
-        *reinterpret_cast<A*>(row + c + 4) = __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 4, 5, 6, 7));
+        put(row + c, __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 0, 1, 2, 3)));
+        put(row + c + 4, __builtin_bit_cast(u32x4, __builtin_shufflevector(v, v, 4, 5, 6, 7)));
       }
     }
   } else {
@@ -209,7 +235,7 @@ __device__ __forceinline__ void store8(T* row, int c, int H, typename Eight<T>::
   }
 }
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const T* x, int64_t ld_x, int x_rows,
                                                                const int32_t* slots, MxqDivisor top_k, int rows, int H,
                                                                T* out, int64_t ld_out, MxqDivisor chunks,
@@ -221,13 +247,13 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const T* x, int64
   const int slot = slots[r];
   const int from = slot < 0 ? -1 : (int)mxq_quot((uint32_t)slot, top_k);
   const bool some = from >= 0 && from < x_rows;
-  store8<T, kVec>(out + (int64_t)r * ld_out, c, H, load8<T, kVec>(x + (some ? from : 0) * ld_x, some ? c : H, H));
+  store8<T, kVec, kStream>(out + (int64_t)r * ld_out, c, H, load8<T, kVec>(x + (some ? from : 0) * ld_x, some ? c : H, H));
 }
 
 // y[t] = sum over the token's slots of weight * row.  One lane per 8 columns of a token.
 constexpr int kAhead = 4;   // rows in flight per lane
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T* rows, int64_t ld_rows, int n_rows,
                                                               const int32_t* position, const float* weights, int top_k,
                                                               int H, T* y, int64_t ld_y, MxqDivisor chunks,
@@ -254,13 +280,13 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T* rows, int
     for (int j = 0; j < kAhead; j++)
       if (some[j]) sum += Eight<T>::widen(v[j]) * w[j];
   }
-  store8<T, kVec>(y + (int64_t)t * ld_y, c, H, Eight<T>::narrow(sum));
+  store8<T, kVec, kStream>(y + (int64_t)t * ld_y, c, H, Eight<T>::narrow(sum));
 }
 
 // Gradients of combine: drows[p] = weight * dy[t], dweights[slot] = <dy[t], rows[p]>.
 // One workgroup per token, so dy is read once for all of the token's slots and
 // the dot products are summed in a fixed order.
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const T* dy, int64_t ld_dy, const T* rows,
                                                                        int64_t ld_rows, int n_rows,
                                                                        const int32_t* position, const float* weights,
@@ -286,7 +312,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const T* 
           for (int i = 0; i < kEPL; i++) dot += d[i] * v[i];
           d *= w;
         }
-        store8<T, kVec>(drows + at * ld_drows, c, H, Eight<T>::narrow(d));
+        store8<T, kVec, kStream>(drows + at * ld_drows, c, H, Eight<T>::narrow(d));
       }
     }
     if (dweights) {
@@ -342,15 +368,15 @@ int mxq_sort_experts(const int32_t* ids, int64_t ld_ids, int64_t n_tokens, int64
   const bool alone = need == 0;
   const int blocks = alone ? 1 : (int)((total + kSortSlots - 1) / kSortSlots);
   const int per_wave = alone ? (int)((total + kSortThreads - 1) / kSortThreads * 64) : kSortSlots / kSortWaves;
-  const SortArgs a{ids,     ld_ids, mxq_divisor((uint32_t)top_k), (int)total, (int)n_experts, per_wave,
-                   offsets, slots,  position,                     alone ? nullptr : (int32_t*)workspace};
+  const SortArgs a{ids,      ld_ids, mxq_divisor((uint32_t)top_k), mxq_divisor((uint32_t)n_experts + 1), (int)total,
+                   (int)n_experts, per_wave, offsets, slots, position, alone ? nullptr : (int32_t*)workspace};
   const uint32_t hist = (uint32_t)(n_experts + 1) * 4;
   if (!alone) {
     hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kSortThreads), hist, stream, a);
     const int st = launch_status();
     if (st != MXQ_OK) return st;
   }
-  hipLaunchKernelGGL(sort_kernel, dim3(blocks), dim3(kSortThreads), hist * kSortWaves, stream, a);
+  hipLaunchKernelGGL(sort_kernel, dim3(blocks), dim3(kSortThreads), hist * (kSortWaves + 2), stream, a);
   return launch_status();
 }
 
@@ -373,13 +399,18 @@ int mxq_dispatch_rows(const void* x, int64_t ld_x, int64_t x_rows, const int32_t
   const bool vec = vector_rows(x, ld_x, dt) && vector_rows(out, ld_out, dt) && H % kEPL == 0;
   const dim3 grid((total + kRowThreads - 1) / kRowThreads), block(kRowThreads);
   const MxqDivisor k = mxq_divisor((uint32_t)top_k);
-#define MXQ_DISPATCH(T, V)                                                                                          \
-  hipLaunchKernelGGL((dispatch_kernel<T, V>), grid, block, 0, stream, (const T*)x, ld_x, (int)x_rows, slots, k,     \
+  const bool stream_out = rows * H * (int64_t)size_of(dt) > kStreamBytes;
+#define MXQ_DISPATCH(T, V, S)                                                                                          \
+  hipLaunchKernelGGL((dispatch_kernel<T, V, S>), grid, block, 0, stream, (const T*)x, ld_x, (int)x_rows, slots, k,     \
                      (int)rows, (int)H, (T*)out, ld_out, chunks, total)
   if (dt == MXQ_BF16) {
-    if (vec) MXQ_DISPATCH(uint16_t, true); else MXQ_DISPATCH(uint16_t, false);
+    if (!vec) MXQ_DISPATCH(uint16_t, false, false);
+    else if (stream_out) MXQ_DISPATCH(uint16_t, true, true);
+    else MXQ_DISPATCH(uint16_t, true, false);
   } else {
-    if (vec) MXQ_DISPATCH(float, true); else MXQ_DISPATCH(float, false);
+    if (!vec) MXQ_DISPATCH(float, false, false);
+    else if (stream_out) MXQ_DISPATCH(float, true, true);
+    else MXQ_DISPATCH(float, true, false);
   }
 #undef MXQ_DISPATCH
   return launch_status();
@@ -407,13 +438,18 @@ int mxq_combine_rows(const void* rows, int64_t ld_rows, int64_t n_rows, const in
   if (!disjoint({ry}, {rr, rp, rw})) return MXQ_ERR_ALIAS;
   const bool vec = vector_rows(rows, ld_rows, dt) && vector_rows(y, ld_y, dt) && H % kEPL == 0;
   const dim3 grid((total + kRowThreads - 1) / kRowThreads), block(kRowThreads);
-#define MXQ_COMBINE(T, V)                                                                                          \
-  hipLaunchKernelGGL((combine_kernel<T, V>), grid, block, 0, stream, (const T*)rows, ld_rows, (int)n_rows,         \
+  const bool stream_out = n_tokens * H * (int64_t)size_of(dt) > kStreamBytes;
+#define MXQ_COMBINE(T, V, S)                                                                                          \
+  hipLaunchKernelGGL((combine_kernel<T, V, S>), grid, block, 0, stream, (const T*)rows, ld_rows, (int)n_rows,         \
                      position, weights, (int)top_k, (int)H, (T*)y, ld_y, chunks, total)
   if (dt == MXQ_BF16) {
-    if (vec) MXQ_COMBINE(uint16_t, true); else MXQ_COMBINE(uint16_t, false);
+    if (!vec) MXQ_COMBINE(uint16_t, false, false);
+    else if (stream_out) MXQ_COMBINE(uint16_t, true, true);
+    else MXQ_COMBINE(uint16_t, true, false);
   } else {
-    if (vec) MXQ_COMBINE(float, true); else MXQ_COMBINE(float, false);
+    if (!vec) MXQ_COMBINE(float, false, false);
+    else if (stream_out) MXQ_COMBINE(float, true, true);
+    else MXQ_COMBINE(float, true, false);
   }
 #undef MXQ_COMBINE
   return launch_status();
@@ -443,13 +479,18 @@ int mxq_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
   const bool vec = vector_rows(dy, ld_dy, dt) && vector_rows(rows, ld_rows, dt) && vector_rows(drows, ld_drows, dt) &&
                    H % kEPL == 0;
   const dim3 grid((uint32_t)n_tokens), block(kRowThreads);
-#define MXQ_BACKWARD(T, V)                                                                                        \
-  hipLaunchKernelGGL((combine_backward_kernel<T, V>), grid, block, 0, stream, (const T*)dy, ld_dy, (const T*)rows, \
+  const bool stream_out = n_rows * H * (int64_t)size_of(dt) > kStreamBytes;
+#define MXQ_BACKWARD(T, V, S)                                                                                        \
+  hipLaunchKernelGGL((combine_backward_kernel<T, V, S>), grid, block, 0, stream, (const T*)dy, ld_dy, (const T*)rows, \
                      ld_rows, (int)n_rows, position, weights, (int)top_k, (int)H, (T*)drows, ld_drows, dweights)
   if (dt == MXQ_BF16) {
-    if (vec) MXQ_BACKWARD(uint16_t, true); else MXQ_BACKWARD(uint16_t, false);
+    if (!vec) MXQ_BACKWARD(uint16_t, false, false);
+    else if (stream_out) MXQ_BACKWARD(uint16_t, true, true);
+    else MXQ_BACKWARD(uint16_t, true, false);
   } else {
-    if (vec) MXQ_BACKWARD(float, true); else MXQ_BACKWARD(float, false);
+    if (!vec) MXQ_BACKWARD(float, false, false);
+    else if (stream_out) MXQ_BACKWARD(float, true, true);
+    else MXQ_BACKWARD(float, true, false);
   }
 #undef MXQ_BACKWARD
   return launch_status();
