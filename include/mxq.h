@@ -51,8 +51,9 @@
  *     Argument errors are detected on the host and returned before anything is
  *     enqueued; no kernel asserts on the device.
  *   - rows == 0 or K == 0 returns MXQ_OK and enqueues nothing.
- *   - Results are bit-exact and do not depend on the build's floating-point
- *     flags: the scale exponents are integer arithmetic on bit patterns, and the
+ *   - Results of the quantizers are bit-exact (the products and the rows'
+ *     weighted sums round as stated at their entry points) and do not depend
+ *     on the build's floating-point flags: the scale exponents are integer arithmetic on bit patterns, and the
  *     kernels set the wave's denormal mode before using the gfx950 scaled
  *     conversions.
  */

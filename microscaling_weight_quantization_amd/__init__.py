@@ -3,8 +3,9 @@
 The ``mxq_*`` functions carry the names of the C entry points in
 ``include/mxq.h`` and only marshal arguments: tensors become device pointers,
 row strides and sizes, and the call is enqueued on torch's current stream.
-Every step of the computation runs in the HIP kernels of ``csrc/mxq.hip``;
-there is no fallback of any kind, and a missing library raises.
+Every step of the computation runs in the HIP kernels of ``csrc/`` (``mxq.hip``;
+``group_quant.hip``, ``product.hip`` and ``experts.hip`` for the FP8 products, their
+operands and the experts' rows); there is no fallback of any kind, and a missing library raises.
 
 PyTorch is used for device memory and streams only.  A [rows, K] operand is a
 tensor whose last dimension is contiguous; leading dimensions of a contiguous

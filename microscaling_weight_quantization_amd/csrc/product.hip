@@ -18,10 +18,17 @@
 //           random bytes, where bf16 output rounds by 2^-9.  The caller asks for
 //           it, and only for activations and their gradients: weight gradients
 //           feed an optimizer, and their segments may be a few rows long.
-//   else    the payloads become bf16, which holds every E4M3 value, and a block is
-//           four v_mfma_f32_16x16x32_bf16, which sum in fp32; the block's sum is
-//           scaled by 2^(codes) exactly and added in fp32.  Half the instruction
-//           rate, and the conversions besides.
+//   else    the payloads become bf16, which holds every E4M3 value, and sum in fp32
+//           at half the instruction rate.  With many rows the codes go into the
+//           conversion to bf16 (exact: they are powers of two) and the sums run
+//           through v_mfma_f32_32x32x16_bf16; with few rows a block is four
+//           v_mfma_f32_16x16x32_bf16, whose sum is scaled and added in fp32.
+//
+// Reached on one MI355X: 8192^3 with kFast 481 us (2280 TFLOP/s; a large library
+// product in FP8 reaches 2659), bound by the clock the card holds under this load;
+// dx of 1.9 TFLOP 845 us; dw of 103 GFLOP over experts with 480 MB of results 237 us
+// (its stores alone 81 us, the rest alone 170); one token through 235 MB of weights
+// 48.2 us (4.9 TB/s), bound by the weights' bytes.
 //
 //   product   i   j   r    V                     U                     U's code
 //   y         m   n   k    x, r contiguous       w, r contiguous       (j / 128, r / 128)
