@@ -8,7 +8,7 @@
 // negative, in both directions (slots[] and position[]).
 //
 // The row kernels are bound by the bytes moved: 605 MB of sort and rows into order
-// take 156 us, 672 MB of rows back and their gradients 121 us (the second kernel
+// take 155 us, 672 MB of rows back and their gradients 120 us (the second kernel
 // finds rows of the first in the last-level cache).  A few tokens' routing is two
 // launches and their calls on the host, 19.6 us.
 #include <hip/hip_runtime.h>

@@ -24,11 +24,11 @@
 //           through v_mfma_f32_32x32x16_bf16; with few rows a block is four
 //           v_mfma_f32_16x16x32_bf16, whose sum is scaled and added in fp32.
 //
-// Reached on one MI355X: 8192^3 with kFast 481 us (2280 TFLOP/s; a large library
+// Reached on one MI355X: 8192^3 with kFast 479 us (2290 TFLOP/s; a large library
 // product in FP8 reaches 2659), bound by the clock the card holds under this load;
-// dx of 1.9 TFLOP 845 us; dw of 103 GFLOP over experts with 480 MB of results 237 us
+// dx of 1.9 TFLOP 832 us; dw of 103 GFLOP over experts with 480 MB of results 237 us
 // (its stores alone 81 us, the rest alone 170); one token through 235 MB of weights
-// 48.2 us (4.9 TB/s), bound by the weights' bytes.
+// 48.1 us (4.9 TB/s), bound by the weights' bytes.
 //
 //   product   i   j   r    V                     U                     U's code
 //   y         m   n   k    x, r contiguous       w, r contiguous       (j / 128, r / 128)
