@@ -39,6 +39,7 @@
 // ds_read_b64_tr_b8 transposes 8 x 16 bytes on the way to the registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "checks.h"
 #include "segments.h"
@@ -699,6 +700,20 @@ struct ByteCodeFeed {
   }
 };
 
+// The same through a register, for code rows so far apart that 64 of them pass a
+// buffer's 32-bit offsets.
+struct ByteCodeCarry {
+  const uint8_t* row;
+  int64_t step;
+  uint32_t next;
+
+  __device__ __forceinline__ ByteCodeCarry(const uint8_t* code, int64_t code_x, int64_t code_r, int shift, int x0, int x_end,
+                                       int)
+      : row(code + (int64_t)(min(x0 + ((int)threadIdx.x & 63), x_end - 1) >> shift) * code_x), step(code_r), next(0) {}
+  __device__ __forceinline__ void fetch(int b) { next = row[b * step]; }
+  __device__ __forceinline__ void store(uint32_t* to) const { to[threadIdx.x & 63] = next; }
+};
+
 // 32 rows' payloads of one block: two halves of 64 reduction indexes.
 struct Rows32 {
   i32x8 h[2];
@@ -805,23 +820,23 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void exact_kernel(Args a,
   const uint8_t* const ud = a.u.data + w.weight * a.u.expert_stride;
   const FV v(a.v.data, a.v.ld, w.i0, w.i_end, w.r_begin, w.r_end);
   const FU u(ud, a.u.ld, w.j0, a.J, w.r_begin, w.r_end);
+  using FC = std::conditional_t<kFed, ByteCodeFeed, ByteCodeCarry>;
+  FC c = wave < BI / 64 ? FC(a.v.code + w.code_block * a.v.code_r, a.v.code_x, a.v.code_r, a.v.x_shift, w.i0 + wave * 64,
+                             w.i_end, blocks)
+                        : FC(a.u.code + w.weight * a.u.code_expert_stride + w.code_block * a.u.code_r, a.u.code_x,
+                             a.u.code_r, a.u.x_shift, w.j0 + (wave - BI / 64) * 64, a.J, blocks);
   Carry<Places<kVContig, BI>, kVContig, BI, kThreads> sv;   // unless kFed
   Carry<Places<kUContig, BJ>, kUContig, BJ, kThreads> su;
   auto fetch = [&](int b) {
     sv.fetch(a.v.data, a.v.ld, w.i0, w.i_end, w.r_begin + b * kR, w.r_end);
     su.fetch(ud, a.u.ld, w.j0, a.J, w.r_begin + b * kR, w.r_end);
+    if constexpr (!kFed) c.fetch(b);
   };
-  const ByteCodeFeed c =
-      wave < BI / 64
-          ? ByteCodeFeed(a.v.code + w.code_block * a.v.code_r, a.v.code_x, a.v.code_r, a.v.x_shift, w.i0 + wave * 64,
-                         w.i_end, blocks)
-          : ByteCodeFeed(a.u.code + w.weight * a.u.code_expert_stride + w.code_block * a.u.code_r, a.u.code_x,
-                         a.u.code_r, a.u.x_shift, w.j0 + (wave - BI / 64) * 64, a.J, blocks);
   const Reader32<kVContig, BI, NI> rv(lds, wi);
   const Reader32<kUContig, BJ, NJ> ru(lds + kVBytes, wj);
   auto load = [&](int b, int stage) {   // past the last block: zeros that nobody reads
     uint8_t* const to = lds + stage * kStage;
-    c.load(lds_address(codes[stage]) + wave * 256, b);
+    if constexpr (kFed) c.load(lds_address(codes[stage]) + wave * 256, b);
     v.load(to, b, w.r_end - w.r_begin - b * kR);
     u.load(to + kVBytes, b, w.r_end - w.r_begin - b * kR);
   };
@@ -842,7 +857,7 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void exact_kernel(Args a,
       load(b + kStages - 1, stage ? stage - 1 : kStages - 1);
     } else {
       // no wave reads block b - 2, whose place this is, since all came here for block b - 1
-      c.load(lds_address(codes[stage]) + wave * 256, b);
+      c.store(codes[stage] + wave * 64);
       sv.store(lds + stage * kStage);
       su.store(lds + stage * kStage + kVBytes);
       arrive();
