@@ -784,10 +784,13 @@ __device__ __forceinline__ Wide64 widen(const Rows32& f, float scale) {
 }
 
 // Sums in fp32 take the codes into the conversion to bf16 where no value can leave
-// bf16's normal range by it and no product fp32's: codes from 77 to 246 (group
-// maxima from about 4e-13 to 3e38).  A block with any other code, 255 among them,
-// is summed unscaled, then scaled exactly.
-constexpr uint32_t kPlainFirst = 77, kPlainLast = 246;
+// bf16's normal range by it and no product or sum fp32's: codes from 77 to 167
+// (group maxima from about 4e-13 to 4.9e14).  The smallest product is then 2^(-18 -
+// 2 * 50), and 2^30 of the largest, 448^2 * 2^(2 * 40), add up to less than 2^128:
+// a sum overflows only if the true one does, and products that cancel do so in
+// fp32.  A block with any other code, 255 among them, is summed unscaled, then scaled
+// exactly, as the few-rows kernels always do.
+constexpr uint32_t kPlainFirst = 77, kPlainLast = 167;
 __device__ __forceinline__ bool plain_code(uint32_t code) { return code - kPlainFirst <= kPlainLast - kPlainFirst; }
 __device__ __forceinline__ float two_to(uint32_t code) { return __builtin_bit_cast(float, code << 23); }
 
