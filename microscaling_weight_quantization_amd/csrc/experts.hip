@@ -30,13 +30,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // A workgroup of 16 waves takes kSlots slots, each wave a run of consecutive
 // ones.  Every wave counts its run's experts in LDS; the counts are summed over
 // waves (and, where there are several workgroups, over the counts that a first
-// launch left in the workspace); then each wave walks its run 64 slots at a
-// time: the lanes that hold the same expert find each other with one ballot for
-// each bit of the id, and a lane's place is the expert's next free one plus the
-// number of such lanes below it.
+// launch left in the workspace: a few of those each workgroup adds up itself, many a
+// launch in between, so that the work stays in proportion to the slots); then
+// each wave walks its run 64 slots at a time: the lanes that hold the same expert
+// find each other with one ballot for each bit of the id, and a lane's place is the
+// expert's next free one plus the number of such lanes below it.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortSlots = 2048;          // slots per workgroup where there are several
 constexpr int kSortAlone = 8192;          // as many as one workgroup takes without a second launch
+// Counts that each workgroup adds up itself.  All of them together read their number
+// times the workgroups, so more are added up once: 2^17 slots for 128 experts (8256
+// counts) take 15 us against 18, 2^18 (16512) 18 against 18, 2^20 for 512 experts
+// (262656) 101 against 29, 2^22 1390 against 81.
+constexpr int64_t kSortDirect = 16384;
 
 __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t ld, MxqDivisor top_k, int slot, int n) {
   const uint32_t t = mxq_quot((uint32_t)slot, top_k);
@@ -52,7 +58,8 @@ struct SortArgs {
   int32_t* offsets;
   int32_t* slots;
   int32_t* position;
-  int32_t* counts;          // [workgroups][n + 1]
+  int32_t* counts;          // [workgroups][n + 1]; null: one workgroup
+  const int32_t* totals;    // [n + 1]: counts are summed over the workgroups before; null: they are not
 };
 
 __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a) {
@@ -64,6 +71,40 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a) {
     atomicAdd(&hist[expert_of(a.ids, a.ld, a.top_k, s, a.n)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e <= a.n; e += kSortThreads) a.counts[(int64_t)blockIdx.x * (a.n + 1) + e] = hist[e];
+}
+
+// Turns each workgroup's counts into the sums over those before it, and leaves the
+// sums over all behind them.  One expert a lane; each wave has a run of workgroups,
+// read twice.
+__global__ __launch_bounds__(kSortThreads) void sums_kernel(int32_t* counts, int groups, int n1) {
+  __shared__ int part[kSortWaves][64];
+  constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, e = blockIdx.x * 64 + lane;
+  const int per = (groups + kSortWaves - 1) / kSortWaves;
+  const int begin = min(wave * per, groups), end = min(begin + per, groups);
+  int32_t* const column = counts + min(e, n1 - 1);
+  int sum = 0;
+#pragma unroll 8
+  for (int g = begin; g < end; g++) sum += column[(int64_t)g * n1];
+  part[wave][lane] = sum;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kSortWaves; w++) {
+    before += w < wave ? part[w][lane] : 0;
+    all += part[w][lane];
+  }
+  if (e >= n1) return;
+  if (wave == 0) column[(int64_t)groups * n1] = all;
+  for (int g0 = begin; g0 < end; g0 += kAhead) {
+    int c[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) c[i] = column[(int64_t)min(g0 + i, end - 1) * n1];
+#pragma unroll
+    for (int i = 0; i < kAhead; i++) {
+      if (g0 + i < end) column[(int64_t)(g0 + i) * n1] = before;
+      before += c[i];
+    }
+  }
 }
 
 // Exclusive sum over the workgroup of one value a lane.
@@ -98,7 +139,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(SortArgs a) {
   // that the first launch left: all lanes at once, added up in LDS
   int* const all = lds + kSortWaves * n1;
   int* const before = all + n1;
-  if (a.counts) {
+  if (a.totals) {
+    for (int e = threadIdx.x; e < n1; e += kSortThreads) {
+      all[e] = a.totals[e];
+      before[e] = a.counts[(int64_t)blockIdx.x * n1 + e];
+    }
+    __syncthreads();
+  } else if (a.counts) {
     for (int e = threadIdx.x; e < 2 * n1; e += kSortThreads) all[e] = 0;
     __syncthreads();
     const int n = (int)gridDim.x * n1, mark = (int)blockIdx.x * n1;
@@ -351,7 +398,9 @@ extern "C" {
 int64_t mxq_sort_experts_workspace(int64_t n_tokens, int64_t top_k, int64_t n_experts) {
   if (n_tokens < 1 || top_k < 1 || n_experts < 1 || top_k > kMaxDim || n_tokens > kMaxDim / top_k) return 0;
   const int64_t total = n_tokens * top_k;
-  return total <= kSortAlone ? 0 : (total + kSortSlots - 1) / kSortSlots * (n_experts + 1) * 4;
+  if (total <= kSortAlone) return 0;
+  const int64_t counts = (total + kSortSlots - 1) / kSortSlots * (n_experts + 1);
+  return (counts + (counts > kSortDirect ? n_experts + 1 : 0)) * 4;
 }
 
 int mxq_sort_experts(const int32_t* ids, int64_t ld_ids, int64_t n_tokens, int64_t top_k, int64_t n_experts,
@@ -372,14 +421,22 @@ int mxq_sort_experts(const int32_t* ids, int64_t ld_ids, int64_t n_tokens, int64
   if (!disjoint({ro, rs, rp, rw}, {ri})) return MXQ_ERR_ALIAS;
   const bool alone = need == 0;
   const int blocks = alone ? 1 : (int)((total + kSortSlots - 1) / kSortSlots);
+  const int64_t counts = blocks * (n_experts + 1);
   const int per_wave = alone ? (int)((total + kSortThreads - 1) / kSortThreads * 64) : kSortSlots / kSortWaves;
   const SortArgs a{ids,      ld_ids, mxq_divisor((uint32_t)top_k), mxq_divisor((uint32_t)n_experts + 1), (int)total,
-                   (int)n_experts, per_wave, offsets, slots, position, alone ? nullptr : (int32_t*)workspace};
+                   (int)n_experts, per_wave, offsets, slots, position, alone ? nullptr : (int32_t*)workspace,
+                   !alone && counts > kSortDirect ? (int32_t*)workspace + counts : nullptr};
   const uint32_t hist = (uint32_t)(n_experts + 1) * 4;
   if (!alone) {
     hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kSortThreads), hist, stream, a);
-    const int st = launch_status();
+    int st = launch_status();
     if (st != MXQ_OK) return st;
+    if (a.totals) {
+      hipLaunchKernelGGL(sums_kernel, dim3((uint32_t)(n_experts + 64) / 64), dim3(kSortThreads), 0, stream, a.counts, blocks,
+                         (int)n_experts + 1);
+      st = launch_status();
+      if (st != MXQ_OK) return st;
+    }
   }
   hipLaunchKernelGGL(sort_kernel, dim3(blocks), dim3(kSortThreads), hist * (kSortWaves + 2), stream, a);
   return launch_status();
