@@ -62,6 +62,10 @@ inline bool all_ok(std::initializer_list<Range> rs) {
 
 inline int launch_status() { return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
 
+// A launch has fewer than 2^32 lanes in a dimension.  Calls that need more go out as
+// launches of up to 2^31: this many rows each, of `lanes` lanes (at most 2^31) a row.
+inline int64_t rows_per_launch(int64_t lanes) { return ((int64_t)1 << 31) / lanes; }
+
 inline bool is_float(mxq_dtype dt) { return dt == MXQ_BF16 || dt == MXQ_FP32; }
 inline size_t size_of(mxq_dtype dt) { return dt == MXQ_BF16 ? 2 : 4; }
 inline int64_t groups_of(int64_t n) { return (n + 127) / 128; }

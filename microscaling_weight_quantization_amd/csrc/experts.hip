@@ -540,22 +540,29 @@ int mxq_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
   if (!disjoint({rd, rv}, {rg, rr, rp, rw})) return MXQ_ERR_ALIAS;
   const bool vec = vector_rows(dy, ld_dy, dt) && vector_rows(rows, ld_rows, dt) && vector_rows(drows, ld_drows, dt) &&
                    H % kEPL == 0;
-  const dim3 grid((uint32_t)n_tokens), block(kRowThreads);
+  const dim3 block(kRowThreads);
   const bool stream_out = n_rows * H * (int64_t)size_of(dt) > kStreamBytes;
 #define MXQ_BACKWARD(T, V, S)                                                                                        \
-  hipLaunchKernelGGL((combine_backward_kernel<T, V, S>), grid, block, 0, stream, (const T*)dy, ld_dy, (const T*)rows, \
-                     ld_rows, (int)n_rows, position, weights, (int)top_k, (int)H, (T*)drows, ld_drows, dweights)
-  if (dt == MXQ_BF16) {
-    if (!vec) MXQ_BACKWARD(uint16_t, false, false);
-    else if (stream_out) MXQ_BACKWARD(uint16_t, true, true);
-    else MXQ_BACKWARD(uint16_t, true, false);
-  } else {
-    if (!vec) MXQ_BACKWARD(float, false, false);
-    else if (stream_out) MXQ_BACKWARD(float, true, true);
-    else MXQ_BACKWARD(float, true, false);
+  hipLaunchKernelGGL((combine_backward_kernel<T, V, S>), grid, block, 0, stream, (const T*)dy + t * ld_dy, ld_dy,     \
+                     (const T*)rows, ld_rows, (int)n_rows, position + t * top_k, weights ? weights + t * top_k : weights, \
+                     (int)top_k, (int)H, (T*)drows, ld_drows, dweights ? dweights + t * top_k : dweights)
+  const int64_t step = rows_per_launch(kRowThreads);
+  for (int64_t t = 0; t < n_tokens; t += step) {
+    const dim3 grid((uint32_t)std::min(step, n_tokens - t));
+    if (dt == MXQ_BF16) {
+      if (!vec) MXQ_BACKWARD(uint16_t, false, false);
+      else if (stream_out) MXQ_BACKWARD(uint16_t, true, true);
+      else MXQ_BACKWARD(uint16_t, true, false);
+    } else {
+      if (!vec) MXQ_BACKWARD(float, false, false);
+      else if (stream_out) MXQ_BACKWARD(float, true, true);
+      else MXQ_BACKWARD(float, true, false);
+    }
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
   }
 #undef MXQ_BACKWARD
-  return launch_status();
+  return MXQ_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,31 @@
+"""Row counts that need more lanes than one launch has (2^32 in a dimension), against torch."""
+import pytest
+import torch
+
+import microscaling_weight_quantization_amd as mxq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def bf16(g, *shape):
+    """Small integers: their products and short sums are exact."""
+    return torch.randint(-4, 5, shape, generator=g, device=DEV, dtype=torch.int16).to(torch.bfloat16)
+
+
+def test_combine_gradients_of_many_tokens():
+    """256 lanes a token."""
+    tokens, H, g = (1 << 24) + 3, 8, gen(1)
+    dy, rows = bf16(g, tokens, H), bf16(g, tokens, H)
+    position = torch.randperm(tokens, generator=g, device=DEV).int().view(tokens, 1)
+    position[5] = ~position[5]
+    w = torch.randint(1, 4, (tokens, 1), generator=g, device=DEV).float()
+    drows, dw = mxq.mxq_combine_rows_backward(dy, rows, position, w)
+    kept = (position >= 0).float()
+    at = torch.where(position >= 0, position, ~position).view(-1).long()
+    assert torch.equal(drows[at].float(), dy.float() * w * kept)
+    assert torch.equal(dw, (dy.float() * rows[at].float()).sum(1, keepdim=True) * kept)
