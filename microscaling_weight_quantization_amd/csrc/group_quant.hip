@@ -318,17 +318,24 @@ bool vector_payload(const uint8_t* p, int64_t ld) { return aligned(p, 8) && ld %
 template <typename T>
 int launch_rows(const Checked& c, int64_t rows, int64_t K, bool vec, uint8_t* data, int64_t ld_data, uint8_t* scale,
                 int64_t scale_ld, hipStream_t stream) {
-  const int64_t groups = groups_of(K), total = rows * groups;
-  if (total > ((int64_t)1 << 31)) return MXQ_ERR_SHAPE;
-  const dim3 grid((uint32_t)((total + kRowThreads / 16 - 1) / (kRowThreads / 16)));
+  const int64_t groups = groups_of(K), step = rows_per_launch(groups * 16);
   const MxqDivisor d = mxq_divisor((uint32_t)groups);
-  if (vec)
-    hipLaunchKernelGGL((row_groups_kernel<T, true>), grid, dim3(kRowThreads), 0, stream, c.src, (int)K, d,
-                       (uint32_t)total, data, ld_data, scale, scale_ld);
-  else
-    hipLaunchKernelGGL((row_groups_kernel<T, false>), grid, dim3(kRowThreads), 0, stream, c.src, (int)K, d,
-                       (uint32_t)total, data, ld_data, scale, scale_ld);
-  return launch_status();
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t total = std::min(step, rows - r) * groups;
+    const dim3 grid((uint32_t)((total + kRowThreads / 16 - 1) / (kRowThreads / 16)));
+    Source src = c.src;   // from row r of the result on
+    if (src.slots) src.slots += r;
+    else src.x = (const T*)src.x + r * src.ld;
+    if (vec)
+      hipLaunchKernelGGL((row_groups_kernel<T, true>), grid, dim3(kRowThreads), 0, stream, src, (int)K, d,
+                         (uint32_t)total, data + r * ld_data, ld_data, scale + r * scale_ld, scale_ld);
+    else
+      hipLaunchKernelGGL((row_groups_kernel<T, false>), grid, dim3(kRowThreads), 0, stream, src, (int)K, d,
+                         (uint32_t)total, data + r * ld_data, ld_data, scale + r * scale_ld, scale_ld);
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
+  }
+  return MXQ_OK;
 }
 
 template <typename T>

@@ -29,3 +29,20 @@ def test_combine_gradients_of_many_tokens():
     at = torch.where(position >= 0, position, ~position).view(-1).long()
     assert torch.equal(drows[at].float(), dy.float() * w * kept)
     assert torch.equal(dw, (dy.float() * rows[at].float()).sum(1, keepdim=True) * kept)
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+def test_quantize_rows_of_many_groups(gathered):
+    """16 lanes a group.  Values on the E4M3 grid: each group's code is its one value's own."""
+    rows, g = (1 << 28) + 9, gen(2)
+    x = torch.randint(0, 127, (rows, 1), generator=g, device=DEV, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    x = x.to(torch.bfloat16)
+    slots = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device=DEV) if gathered else None
+    q, codes = mxq.mxq_quantize_fp8_group128(x, slots=slots)
+    if gathered:
+        x = x.flip(0)
+    for lo in range(0, rows, 1 << 26):           # a part at a time: the values in 64 bits are 8 bytes each
+        part = slice(lo, min(rows, lo + (1 << 26)))
+        value = q[part].view(torch.float8_e4m3fn).double() * torch.exp2(codes[part].double() - 127)
+        assert torch.equal(value, x[part].double())
+        assert bool(((codes[part] == 0) == (x[part] == 0)).all())
