@@ -190,13 +190,13 @@ constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 
 template <typename T, bool kVec, bool kRow, bool kStream>
 __global__ __launch_bounds__(kTileThreads) void tile_groups_kernel(
-    Source src, int rows, int K, const int32_t* offsets, int experts, int code_rows, uint8_t* row_data,
+    Source src, int first_id, int rows, int K, const int32_t* offsets, int experts, int code_rows, uint8_t* row_data,
     int64_t ld_row, uint8_t* row_scale, int64_t row_scale_ld, uint8_t* col_data, int64_t ld_col, uint8_t* col_scale,
     int64_t col_scale_ld) {
   keep_denormals();
   __shared__ uint32_t part[kTileThreads / 64][kGroup];
   const int lane16 = threadIdx.x & 15, row16 = threadIdx.x / 16, wave = threadIdx.x / 64;
-  const int id = blockIdx.y, c = blockIdx.x * kGroup + lane16 * kEPL;
+  const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup + lane16 * kEPL;
   Segment s{0, id, 0, rows, 0};
   if (offsets) s = mxq_dev::find_tile<kGroup>(offsets, experts, rows, id);
   const bool owned = !offsets || s.expert < experts;
@@ -343,24 +343,29 @@ int launch_tiles(const Checked& c, int64_t rows, int64_t K, bool vec, const int3
                  int64_t code_rows, uint8_t* row_data, int64_t ld_row, uint8_t* row_scale, int64_t row_scale_ld,
                  uint8_t* col_data, int64_t ld_col, uint8_t* col_scale, int64_t col_scale_ld, hipStream_t stream) {
   const int64_t tiles = code_rows + (offsets ? 2 : 0);   // the rows of no expert, behind and before the others, may take two more
-  if (tiles > 65535) return MXQ_ERR_SHAPE;
-  const dim3 grid((uint32_t)groups_of(K), (uint32_t)tiles), block(kTileThreads);
+  constexpr int64_t kStep = 65535;   // of a grid's second dimension
+  const dim3 block(kTileThreads);
 #define MXQ_TILE_LAUNCH(V, R, S)                                                                                      \
-  hipLaunchKernelGGL((tile_groups_kernel<T, V, R, S>), grid, block, 0, stream, c.src, (int)rows, (int)K, offsets,     \
+  hipLaunchKernelGGL((tile_groups_kernel<T, V, R, S>), grid, block, 0, stream, c.src, (int)t, (int)rows, (int)K, offsets, \
                      (int)experts, (int)code_rows, row_data, ld_row, row_scale, row_scale_ld, col_data, ld_col,    \
                      col_scale, col_scale_ld)
   const bool big = rows * K > kStreamBytes;
-  if (row_data) {
-    if (!vec) MXQ_TILE_LAUNCH(false, true, false);
-    else if (big) MXQ_TILE_LAUNCH(true, true, true);
-    else MXQ_TILE_LAUNCH(true, true, false);
-  } else {
-    if (!vec) MXQ_TILE_LAUNCH(false, false, false);
-    else if (big) MXQ_TILE_LAUNCH(true, false, true);
-    else MXQ_TILE_LAUNCH(true, false, false);
+  for (int64_t t = 0; t < tiles; t += kStep) {
+    const dim3 grid((uint32_t)groups_of(K), (uint32_t)std::min(kStep, tiles - t));
+    if (row_data) {
+      if (!vec) MXQ_TILE_LAUNCH(false, true, false);
+      else if (big) MXQ_TILE_LAUNCH(true, true, true);
+      else MXQ_TILE_LAUNCH(true, true, false);
+    } else {
+      if (!vec) MXQ_TILE_LAUNCH(false, false, false);
+      else if (big) MXQ_TILE_LAUNCH(true, false, true);
+      else MXQ_TILE_LAUNCH(true, false, false);
+    }
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
   }
 #undef MXQ_TILE_LAUNCH
-  return launch_status();
+  return MXQ_OK;
 }
 
 int tile_entry(const void* x, int64_t ld_x, int64_t x_rows, int64_t rows, int64_t K, mxq_dtype dt,

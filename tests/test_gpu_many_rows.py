@@ -46,3 +46,29 @@ def test_quantize_rows_of_many_groups(gathered):
         value = q[part].view(torch.float8_e4m3fn).double() * torch.exp2(codes[part].double() - 127)
         assert torch.equal(value, x[part].double())
         assert bool(((codes[part] == 0) == (x[part] == 0)).all())
+
+
+@pytest.mark.parametrize("experts", [0, 3])
+def test_quantize_columns_of_many_rows(experts):
+    """More than 65535 tiles of 128 rows, by expert or not."""
+    rows, K, g = 65536 * 128 * 2 + 300, 3, gen(3)
+    x = torch.randint(0, 127, (rows, K), generator=g, device=DEV, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    x = x.to(torch.bfloat16)
+    ends = [0, 77, rows // 2 + 1, rows - 5] if experts else [0, rows]
+    offsets = torch.tensor(ends, dtype=torch.int32, device=DEV) if experts else None
+    rq, rc, q, codes = mxq.mxq_quantize_fp8_group128_row_col(x, offsets=offsets)
+    q2, codes2 = mxq.mxq_quantize_fp8_group128_col(x, offsets=offsets)
+    assert torch.equal(q, q2) and torch.equal(codes, codes2)
+    one = mxq.mxq_quantize_fp8_group128(x)
+    assert torch.equal(rq, one[0]) and torch.equal(rc, one[1])
+    first = 0
+    for lo, hi in zip(ends, ends[1:]):           # each expert's groups, transposed, are a row's
+        n = (hi - lo + 127) // 128
+        part = torch.zeros((n * 128, K), dtype=x.dtype, device=DEV)
+        part[:hi - lo] = x[lo:hi]
+        groups = part.view(n, 128, K).transpose(1, 2).reshape(n * K, 128).contiguous()
+        wq, wc = mxq.mxq_quantize_fp8_group128(groups)
+        assert torch.equal(codes[first:first + n], wc.view(n, K))
+        assert torch.equal(q[lo:hi], wq.view(n, K, 128).transpose(1, 2).reshape(n * 128, K)[:hi - lo])
+        first += n
+    assert (codes[first:] == 0).all() and (q[ends[-1]:] == 0).all()
