@@ -289,7 +289,7 @@ __device__ __forceinline__ void store8(T* row, int c, int H, typename Eight<T>::
 
 template <typename T, bool kVec, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const T* x, int64_t ld_x, int x_rows,
-                                                               const int32_t* slots, MxqDivisor top_k, int rows, int H,
+                                                               const int32_t* slots, MxqDivisor top_k, int H,
                                                                T* out, int64_t ld_out, MxqDivisor chunks,
                                                                uint32_t total) {
   const uint32_t g = blockIdx.x * kRowThreads + threadIdx.x;
@@ -382,14 +382,9 @@ bool vector_rows(const void* p, int64_t ld, mxq_dtype dt) {
   return aligned(p, 16) && ld % (16 / (int64_t)size_of(dt)) == 0;
 }
 
-// Lanes of 8 columns over `rows` rows; false where they are too many for one launch.
-bool lanes_for(int64_t rows, int64_t H, MxqDivisor* chunks, uint32_t* total) {
-  const int64_t per = (H + kEPL - 1) / kEPL;
-  if (rows > ((int64_t)1 << 31) / per) return false;
-  *chunks = mxq_divisor((uint32_t)per);
-  *total = (uint32_t)(rows * per);
-  return true;
-}
+// Lanes of a row, 8 columns each.
+int64_t lanes_of(int64_t H) { return (H + kEPL - 1) / kEPL; }
+dim3 grid_for(int64_t rows, int64_t H) { return dim3((uint32_t)((rows * lanes_of(H) + kRowThreads - 1) / kRowThreads)); }
 
 }  // namespace
 
@@ -452,30 +447,34 @@ int mxq_dispatch_rows(const void* x, int64_t ld_x, int64_t x_rows, const int32_t
   if (ld_x < H || ld_out < H) return MXQ_ERR_SHAPE;
   const Range rx = matrix_range(x, x_rows, H, ld_x, size_of(dt)), rs = matrix_range(slots, 1, rows, rows, 4),
               ro = matrix_range(out, rows, H, ld_out, size_of(dt));
-  MxqDivisor chunks;
-  uint32_t total;
-  if (!all_ok({rx, rs, ro}) || !aligned(slots, 4) || !aligned(x, size_of(dt)) || !aligned(out, size_of(dt)) ||
-      !lanes_for(rows, H, &chunks, &total))
+  if (!all_ok({rx, rs, ro}) || !aligned(slots, 4) || !aligned(x, size_of(dt)) || !aligned(out, size_of(dt)))
     return MXQ_ERR_SHAPE;
   if (!disjoint({ro}, {rx, rs})) return MXQ_ERR_ALIAS;
   const bool vec = vector_rows(x, ld_x, dt) && vector_rows(out, ld_out, dt) && H % kEPL == 0;
-  const dim3 grid((total + kRowThreads - 1) / kRowThreads), block(kRowThreads);
-  const MxqDivisor k = mxq_divisor((uint32_t)top_k);
+  const dim3 block(kRowThreads);
+  const MxqDivisor k = mxq_divisor((uint32_t)top_k), chunks = mxq_divisor((uint32_t)lanes_of(H));
   const bool stream_out = rows * H * (int64_t)size_of(dt) > kStreamBytes;
 #define MXQ_DISPATCH(T, V, S)                                                                                          \
-  hipLaunchKernelGGL((dispatch_kernel<T, V, S>), grid, block, 0, stream, (const T*)x, ld_x, (int)x_rows, slots, k,     \
-                     (int)rows, (int)H, (T*)out, ld_out, chunks, total)
-  if (dt == MXQ_BF16) {
-    if (!vec) MXQ_DISPATCH(uint16_t, false, false);
-    else if (stream_out) MXQ_DISPATCH(uint16_t, true, true);
-    else MXQ_DISPATCH(uint16_t, true, false);
-  } else {
-    if (!vec) MXQ_DISPATCH(float, false, false);
-    else if (stream_out) MXQ_DISPATCH(float, true, true);
-    else MXQ_DISPATCH(float, true, false);
+  hipLaunchKernelGGL((dispatch_kernel<T, V, S>), grid, block, 0, stream, (const T*)x, ld_x, (int)x_rows, slots + r, k, \
+                     (int)H, (T*)out + r * ld_out, ld_out, chunks, (uint32_t)(n * lanes_of(H)))
+  const int64_t step = rows_per_launch(lanes_of(H));
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t n = std::min(step, rows - r);
+    const dim3 grid = grid_for(n, H);
+    if (dt == MXQ_BF16) {
+      if (!vec) MXQ_DISPATCH(uint16_t, false, false);
+      else if (stream_out) MXQ_DISPATCH(uint16_t, true, true);
+      else MXQ_DISPATCH(uint16_t, true, false);
+    } else {
+      if (!vec) MXQ_DISPATCH(float, false, false);
+      else if (stream_out) MXQ_DISPATCH(float, true, true);
+      else MXQ_DISPATCH(float, true, false);
+    }
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
   }
 #undef MXQ_DISPATCH
-  return launch_status();
+  return MXQ_OK;
 }
 
 int mxq_combine_rows(const void* rows, int64_t ld_rows, int64_t n_rows, const int32_t* position, const float* weights,
@@ -492,29 +491,36 @@ int mxq_combine_rows(const void* rows, int64_t ld_rows, int64_t n_rows, const in
   const Range rr = matrix_range(rows, n_rows, H, ld_rows, size_of(dt)), rp = matrix_range(position, 1, slots, slots, 4),
               rw = matrix_range(weights, 1, weights ? slots : 0, slots, 4),
               ry = matrix_range(y, n_tokens, H, ld_y, size_of(dt));
-  MxqDivisor chunks;
-  uint32_t total;
   if (!all_ok({rr, rp, rw, ry}) || !aligned(position, 4) || !aligned(weights, 4) || !aligned(rows, size_of(dt)) ||
-      !aligned(y, size_of(dt)) || !lanes_for(n_tokens, H, &chunks, &total))
+      !aligned(y, size_of(dt)))
     return MXQ_ERR_SHAPE;
   if (!disjoint({ry}, {rr, rp, rw})) return MXQ_ERR_ALIAS;
   const bool vec = vector_rows(rows, ld_rows, dt) && vector_rows(y, ld_y, dt) && H % kEPL == 0;
-  const dim3 grid((total + kRowThreads - 1) / kRowThreads), block(kRowThreads);
+  const dim3 block(kRowThreads);
+  const MxqDivisor chunks = mxq_divisor((uint32_t)lanes_of(H));
   const bool stream_out = n_tokens * H * (int64_t)size_of(dt) > kStreamBytes;
 #define MXQ_COMBINE(T, V, S)                                                                                          \
   hipLaunchKernelGGL((combine_kernel<T, V, S>), grid, block, 0, stream, (const T*)rows, ld_rows, (int)n_rows,         \
-                     position, weights, (int)top_k, (int)H, (T*)y, ld_y, chunks, total)
-  if (dt == MXQ_BF16) {
-    if (!vec) MXQ_COMBINE(uint16_t, false, false);
-    else if (stream_out) MXQ_COMBINE(uint16_t, true, true);
-    else MXQ_COMBINE(uint16_t, true, false);
-  } else {
-    if (!vec) MXQ_COMBINE(float, false, false);
-    else if (stream_out) MXQ_COMBINE(float, true, true);
-    else MXQ_COMBINE(float, true, false);
+                     position + t * top_k, weights ? weights + t * top_k : weights, (int)top_k, (int)H,               \
+                     (T*)y + t * ld_y, ld_y, chunks, (uint32_t)(n * lanes_of(H)))
+  const int64_t step = rows_per_launch(lanes_of(H));
+  for (int64_t t = 0; t < n_tokens; t += step) {
+    const int64_t n = std::min(step, n_tokens - t);
+    const dim3 grid = grid_for(n, H);
+    if (dt == MXQ_BF16) {
+      if (!vec) MXQ_COMBINE(uint16_t, false, false);
+      else if (stream_out) MXQ_COMBINE(uint16_t, true, true);
+      else MXQ_COMBINE(uint16_t, true, false);
+    } else {
+      if (!vec) MXQ_COMBINE(float, false, false);
+      else if (stream_out) MXQ_COMBINE(float, true, true);
+      else MXQ_COMBINE(float, true, false);
+    }
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
   }
 #undef MXQ_COMBINE
-  return launch_status();
+  return MXQ_OK;
 }
 
 int mxq_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, int64_t ld_rows, int64_t n_rows,

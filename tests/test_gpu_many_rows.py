@@ -72,3 +72,19 @@ def test_quantize_columns_of_many_rows(experts):
         assert torch.equal(q[lo:hi], wq.view(n, K, 128).transpose(1, 2).reshape(n * 128, K)[:hi - lo])
         first += n
     assert (codes[first:] == 0).all() and (q[ends[-1]:] == 0).all()
+
+
+def test_many_wide_rows_into_order_and_back():
+    """More than 2^34 elements of the result, at 8 a lane."""
+    rows, H, few, g = (1 << 21) + 3, 8192, 1000, gen(4)
+    x, at = bf16(g, few, H), torch.randint(0, few, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    at[17] = -1
+    for name in ("dispatch", "combine"):
+        out = mxq.mxq_dispatch_rows(x, at, 1) if name == "dispatch" else mxq.mxq_combine_rows(x, at.view(rows, 1))
+        assert (out[17] == 0).all()
+        for lo in range(0, rows, 1 << 17):
+            part = slice(lo, min(rows, lo + (1 << 17)))
+            want = x[at[part].clamp(min=0).long()]
+            want[at[part] < 0] = 0
+            assert torch.equal(out[part], want), f"{name}, rows from {lo}"
+        del out
