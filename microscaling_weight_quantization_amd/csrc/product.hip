@@ -39,6 +39,7 @@
 // ds_read_b64_tr_b8 transposes 8 x 16 bytes on the way to the registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <algorithm>
 #include <type_traits>
 
 #include "checks.h"
@@ -368,7 +369,7 @@ struct Carry {
 };
 
 template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void carried_kernel(Args a) {
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void carried_kernel(Args a, int tj) {
   constexpr int kThreads = BI / WI * (BJ / WJ) * 64;
   constexpr bool kUContig = kMode == kForward;
   using TV = Tile<true, BI>;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void carried_kernel(Args 
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
   const int wi = wave / (BJ / WJ) * WI, wj = wave % (BJ / WJ) * WJ;
-  const Work w = work_of<kMode, BI, BJ>(a, blockIdx.y, blockIdx.x);
+  const Work w = work_of<kMode, BI, BJ>(a, blockIdx.x / tj, blockIdx.x % tj);
   if (w.none) return;
   const uint8_t* const ud = a.u.data + w.weight * a.u.expert_stride;
   const uint8_t* const uc = a.u.code + w.weight * a.u.code_expert_stride;
@@ -425,9 +426,8 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void carried_kernel(Args 
 template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ>
 int launch_carried(const Args& a, hipStream_t stream) {
   const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ, ti = a.offsets ? a.I / BI + a.experts + 2 : ((int64_t)a.I + BI - 1) / BI;
-  if (ti > 65535) return MXQ_ERR_SHAPE;
-  hipLaunchKernelGGL((carried_kernel<kMode, TO, BI, BJ, WI, WJ>), dim3((uint32_t)tj, (uint32_t)ti),
-                     dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a);
+  hipLaunchKernelGGL((carried_kernel<kMode, TO, BI, BJ, WI, WJ>), dim3((uint32_t)(ti * tj)),
+                     dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)tj);
   return launch_status();
 }
 
@@ -656,7 +656,6 @@ template <Mode kMode, typename TO, int BI, int BJ, int WI, int WJ, int kStages>
 int launch_tiles(const Args& a, hipStream_t stream) {
   const int64_t tj = ((int64_t)a.J + BJ - 1) / BJ;
   const int64_t ti = a.offsets ? a.I / BI + a.experts + 2 : ((int64_t)a.I + BI - 1) / BI;
-  if (ti * tj > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
   hipLaunchKernelGGL((tile_kernel<kMode, TO, BI, BJ, WI, WJ, kStages>), dim3((uint32_t)(ti * tj)),
                      dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)ti, (int)tj);
   return launch_status();
@@ -964,7 +963,6 @@ int launch_exact(const Args& a, hipStream_t stream) {
     if (kMode == kWgrad) tz = a.experts;
     else ti = a.I / BI + a.experts + 2;
   }
-  if (ti * tj > 0x7FFFFFFF) return MXQ_ERR_SHAPE;
   hipLaunchKernelGGL((exact_kernel<kMode, kFed, TO, BI, BJ, WI, WJ, kStages>), dim3((uint32_t)(ti * tj), 1, (uint32_t)tz),
                      dim3(BI / WI * (BJ / WJ) * 64), 0, stream, a, (int)ti, (int)tj);
   return launch_status();
@@ -1155,7 +1153,7 @@ template <Mode kMode, bool kFast, int kNI, int kNJ>
 int launch_few(const Args& a, hipStream_t stream) {
   const int64_t tj = ((int64_t)a.J + 16 * kNJ - 1) / (16 * kNJ);
   const int64_t ti = a.offsets ? a.I / (16 * kNI) + a.experts + 2 : ((int64_t)a.I + 16 * kNI - 1) / (16 * kNI);
-  if (ti > 65535) return MXQ_ERR_SHAPE;
+  if (ti > 65535) return MXQ_ERR_SHAPE;   // launch() sends so many rows elsewhere
   const dim3 grid((uint32_t)tj, (uint32_t)ti);
   // Eight waves a workgroup where the workgroups do not fill the card (one row x
   // 8192 x 8192: 20.9 us, with four 26.7), else four, which leave less of a wave's
@@ -1268,12 +1266,30 @@ bool vector_out(const void* out, int64_t ld, int64_t stride, mxq_dtype dt) {
 }
 
 template <Mode kMode>
-int dispatch(const Args& a, bool fast, mxq_dtype out_dt, hipStream_t stream) {
+int dispatch_columns(const Args& a, bool fast, hipStream_t stream) {
   if constexpr (kMode != kWgrad) {
-    if (fast)
-      return out_dt == MXQ_BF16 ? launch<kMode, true, __bf16>(a, stream) : launch<kMode, true, float>(a, stream);
+    if (fast) return a.out_bf16 ? launch<kMode, true, __bf16>(a, stream) : launch<kMode, true, float>(a, stream);
   }
-  return out_dt == MXQ_BF16 ? launch<kMode, false, __bf16>(a, stream) : launch<kMode, false, float>(a, stream);
+  return a.out_bf16 ? launch<kMode, false, __bf16>(a, stream) : launch<kMode, false, float>(a, stream);
+}
+
+// A launch has fewer than 2^32 lanes in a dimension: outputs of more than 2^22
+// tiles of 128 x 128, or of more than 2^28 columns, are made some columns at a time.
+template <Mode kMode>
+int dispatch(const Args& a, bool fast, hipStream_t stream) {
+  const int64_t ti = a.offsets && kMode != kWgrad ? a.I / 128 + a.experts + 2 : ((int64_t)a.I + 127) / 128;
+  const int64_t tj = std::min(std::max((int64_t)1, ((int64_t)1 << 22) / ti), (int64_t)1 << 21), step = tj * 128;
+  if (a.J <= step) return dispatch_columns<kMode>(a, fast, stream);
+  for (int64_t j = 0; j < a.J; j += step) {
+    Args part = a;
+    part.J = (int)std::min(step, a.J - j);
+    part.u.data += kMode == kForward ? j * a.u.ld : j;
+    part.u.code += (j >> a.u.x_shift) * a.u.code_x;
+    part.out = (uint8_t*)a.out + j * (a.out_bf16 ? 2 : 4);
+    const int st = dispatch_columns<kMode>(part, fast, stream);
+    if (st != MXQ_OK) return st;
+  }
+  return MXQ_OK;
 }
 
 }  // namespace
@@ -1294,7 +1310,7 @@ int mxq_matmul_fp8_block128(const uint8_t* x, int64_t ld_x, const uint8_t* x_sca
   const Args a{Operand{x, ld_x, 0, x_scale, x_scale_ld, 1, 0, 0},
                Operand{w, ld_w, w_stride, tile_code, tile_ld, 1, tile_stride, 7},
                out, ld_out, 0, offsets, (int)n, (int)M, (int)N, (int)K, vector_out(out, ld_out, 0, out_dt), out_dt == MXQ_BF16};
-  return dispatch<kForward>(a, fast_accum != 0, out_dt, stream);
+  return dispatch<kForward>(a, fast_accum != 0, stream);
 }
 
 int mxq_matmul_fp8_block128_dgrad(const uint8_t* dy, int64_t ld_dy, const uint8_t* dy_scale, int64_t dy_scale_ld,
@@ -1311,7 +1327,7 @@ int mxq_matmul_fp8_block128_dgrad(const uint8_t* dy, int64_t ld_dy, const uint8_
   const Args a{Operand{dy, ld_dy, 0, dy_scale, dy_scale_ld, 1, 0, 0},
                Operand{w, ld_w, w_stride, tile_code, 1, tile_ld, tile_stride, 7},
                dx, ld_dx, 0, offsets, (int)n, (int)M, (int)K, (int)N, vector_out(dx, ld_dx, 0, out_dt), out_dt == MXQ_BF16};
-  return dispatch<kDgrad>(a, fast_accum != 0, out_dt, stream);
+  return dispatch<kDgrad>(a, fast_accum != 0, stream);
 }
 
 int mxq_matmul_fp8_group128_wgrad(const uint8_t* dy, int64_t ld_dy, const uint8_t* dy_scale, int64_t dy_scale_ld,
@@ -1328,7 +1344,7 @@ int mxq_matmul_fp8_group128_wgrad(const uint8_t* dy, int64_t ld_dy, const uint8_
                Operand{x, ld_x, 0, x_scale, 1, x_scale_ld, 0, 0},
                dw, ld_dw, dw_stride, offsets, (int)n, (int)N, (int)K, (int)M,
                vector_out(dw, ld_dw, n > 1 ? dw_stride : 0, out_dt), out_dt == MXQ_BF16};
-  return dispatch<kWgrad>(a, false, out_dt, stream);
+  return dispatch<kWgrad>(a, false, stream);
 }
 
 }  // extern "C"

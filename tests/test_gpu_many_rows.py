@@ -88,3 +88,45 @@ def test_many_wide_rows_into_order_and_back():
             want[at[part] < 0] = 0
             assert torch.equal(out[part], want), f"{name}, rows from {lo}"
         del out
+
+
+def e4m3(g, *shape):
+    """Small integers in E4M3."""
+    return torch.randint(-4, 5, shape, generator=g, device=DEV, dtype=torch.int16).to(torch.float32).to(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("fast", [False, True])
+def test_products_of_many_rows(fast):
+    """More than 65535 tiles of 128 rows that begin at odd addresses."""
+    M, N, K, g = 65536 * 128 + 5, 70, 17, gen(5)
+    x, w = e4m3(g, M, K), e4m3(g, N, K)
+    one = lambda *s: torch.full(s, 127, dtype=torch.uint8, device=DEV)
+    y = mxq.mxq_matmul_fp8_block128(x, one(M, 1), w, one(1, 1), out_dtype=torch.float32, fast_accum=fast)
+    assert torch.equal(y, x.float() @ w.float().t())
+    dx = mxq.mxq_matmul_fp8_block128_dgrad(x, one(M, 1), w.t().contiguous(), one(1, 1), out_dtype=torch.float32,
+                                           fast_accum=fast)
+    assert torch.equal(dx, y)
+
+
+@pytest.mark.parametrize("fast", [False, True])
+def test_products_of_many_columns(fast):
+    """2^29 columns and more, at 8 lanes a column."""
+    J, g = (1 << 29) + 200, gen(6)
+    x, w = e4m3(g, 1, 1), e4m3(g, J, 1)
+    x[0, 0] = 3
+    tiles = torch.randint(120, 131, ((J + 127) // 128, 1), generator=g, device=DEV, dtype=torch.uint8)
+    one = torch.full((1, 1), 127, dtype=torch.uint8, device=DEV)
+    y = mxq.mxq_matmul_fp8_block128(x, one, w, tiles, fast_accum=fast)
+    dx = mxq.mxq_matmul_fp8_block128_dgrad(x, one, w.t(), tiles.t(), fast_accum=fast)
+    for lo in range(0, J, 1 << 26):
+        part = slice(lo, min(J, lo + (1 << 26)))
+        scale = torch.exp2(tiles[lo // 128:(part.stop + 127) // 128].float() - 127).repeat_interleave(128)[:part.stop - lo]
+        want = (3 * w[part, 0].float() * scale).bfloat16()
+        assert torch.equal(y[0, part], want) and torch.equal(dx[0, part], want), f"columns from {lo}"
+    if not fast:
+        codes = torch.randint(120, 131, (1, J), generator=g, device=DEV, dtype=torch.uint8)
+        dw = mxq.mxq_matmul_fp8_group128_wgrad(x, one, w.t(), codes, out_dtype=torch.bfloat16)
+        for lo in range(0, J, 1 << 26):
+            part = slice(lo, min(J, lo + (1 << 26)))
+            want = (3 * w[part, 0].float() * torch.exp2(codes[0, part].float() - 127)).bfloat16()
+            assert torch.equal(dw[0, part], want), f"columns from {lo}"
