@@ -445,8 +445,10 @@ int launch_carried(const Args& a, hipStream_t stream) {
 // 2^31 - 1 of them; offsets at or past its end read zeros.  A wave's lanes write
 // consecutive words (or 16 bytes each) from the LDS address `to` on.  These are
 // instructions and not the compiler's builtins, which would wait for them before
-// every later LDS read; they have no output register.  arrive() waits for this
-// wave's and then for the workgroup's.
+// every later LDS read; they have no output register.  They say that m0 is written
+// (a reserved register, which the compiler remarks on), so that no value of the
+// compiler's own is taken to live on in it.  arrive() waits for this wave's and then
+// for the workgroup's.
 constexpr int kPastEnd = 0x7FFFFFFF;
 __device__ __forceinline__ i32x4 buffer(const uint8_t* base, int64_t left) {
   const uint64_t p = (uint64_t)base;
@@ -455,15 +457,18 @@ __device__ __forceinline__ i32x4 buffer(const uint8_t* base, int64_t left) {
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 #define MXQ_LOAD_TO_LDS(name, instruction)                                                             \
   __device__ __forceinline__ void name(i32x4 from, uint32_t to, int off) {                             \
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t" instruction " %0, %1, 0 offen lds" ::"v"(off), "s"(from), "s"(to) \
-                 : "memory");                                                                          \
+                 : "m0", "memory");                                                                    \
   }
 MXQ_LOAD_TO_LDS(load_to_lds_16, "buffer_load_dwordx4")
 MXQ_LOAD_TO_LDS(load_to_lds_4, "buffer_load_dword")
 MXQ_LOAD_TO_LDS(load_to_lds_1, "buffer_load_ubyte")
 #undef MXQ_LOAD_TO_LDS
+#pragma clang diagnostic pop
 // Waits for this wave's loads to LDS but the last kLeft, then for the workgroup.
 template <int kLeft>
 __device__ __forceinline__ void arrive_but() {
