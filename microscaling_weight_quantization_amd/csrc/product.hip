@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "checks.h"
+#include "product_choice.h"
 #include "segments.h"
 
 namespace {
@@ -64,7 +65,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 #define MXQ_LDS(T, p) ((__attribute__((address_space(3))) T*)(p))
 
 constexpr int kR = 128;   // the reduction block: one group, one product instruction
-constexpr int64_t kCUs = 256;
 
 struct Operand {
   const uint8_t* data;
@@ -75,8 +75,6 @@ struct Operand {
   int64_t code_expert_stride;
   int x_shift;               // 7: one code for 128 rows of U, 0: one for each
 };
-
-enum Mode { kForward, kDgrad, kWgrad };
 
 struct Args {
   Operand v, u;
@@ -1174,50 +1172,22 @@ int launch_few(const Args& a, hipStream_t stream) {
   return launch_status();
 }
 
-// Tiles of B x B outputs that have rows, as far as the host can tell: it does not
-// read the offsets, and takes every expert to have its share.
-int64_t tiles_of(const Args& a, int64_t B) {
-  const int64_t ti = a.offsets ? a.I / B + (a.I < a.experts ? a.I : a.experts) : (a.I + B - 1) / B;
-  return ti * ((a.J + B - 1) / B);
-}
-
-// Which kernel a product takes.  All compute the same sums; the choice is made on
-// sizes and alignment alone, from sweeps over 1 to 3000 rows, 1024 to 28672
-// columns and 8 to 128 experts.
 template <Mode kMode, bool kFast, typename TO>
 int launch(const Args& a, hipStream_t stream) {
   const bool fed = feedable(a.v, kMode == kWgrad ? a.I : a.R, 0) && feedable(a.u, kMode == kForward ? a.R : a.J, a.experts);
+  const ProductKernel kernel = choose_kernel(kMode, kFast, fed, a.I, a.J, a.offsets ? a.experts : 0);
   if constexpr (kMode != kWgrad) {
-    // Rows that meet one weight: all of them, or an expert's share.
-    const int64_t rows = a.offsets ? (a.I + a.experts - 1) / a.experts : a.I;
-    // The few-rows kernels read V anew for every 64 columns and U for every 64
-    // rows, so they are the faster ones while they make about one workgroup for
-    // each CU (192 rows x 4096 x 4096: 25.7 us against 29.3 in tiles; 192 x 8192 x
-    // 8192: 83.7 against 53.0), or, where 128 x 128 tiles fill the card, up to 8
-    // rows (y with FP8 sums: 5 rows each for 48 experts 19.4 against 21.5, 12 rows
-    // 26.1 against 23.6), none (dx: 1 row 18.9 against 13.7) or 32 (sums in fp32: 25
-    // rows 39 against 45, 40 rows 69 against 45).  Unaligned rows reach the tiles
-    // through registers, so the few-rows kernels hold out for twice as many.
-    const int64_t step = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    const int64_t groups = ((a.J + 63) / 64) * (a.offsets ? a.experts * ((rows + step - 1) / step) : (rows + step - 1) / step);
-    const bool full = tiles_of(a, 128) >= kCUs * 3 / 4;
-    const int64_t most = !kFast ? 32 : kMode == kForward ? 8 : 0;
-    if (!fed ? rows <= 16 || groups <= 2 * kCUs : full ? rows <= most : groups <= kCUs) {
-      if (step == 16) return launch_few<kMode, kFast, 1, kMode == kDgrad ? 8 : 4>(a, stream);
-      if (step == 32) return launch_few<kMode, kFast, 2, 4>(a, stream);
-      return launch_few<kMode, kFast, 4, 4>(a, stream);
-    }
+    if (kernel == kFewRows16) return launch_few<kMode, kFast, 1, kMode == kDgrad ? 8 : 4>(a, stream);
+    if (kernel == kFewRows32) return launch_few<kMode, kFast, 2, 4>(a, stream);
+    if (kernel == kFewRows64) return launch_few<kMode, kFast, 4, 4>(a, stream);
   }
   if constexpr (kFast) {
-    if (!fed) return launch_carried<kMode, TO, 128, 128, 64, 64>(a, stream);
-    // A CU has one 256 x 256 tile or two of 128 x 128 at a time.  A round of the
-    // former takes 1.8 us for each reduction block, one of the latter 1.1 us.
-    const int64_t big = (tiles_of(a, 256) + kCUs - 1) / kCUs, small = (tiles_of(a, 128) + 2 * kCUs - 1) / (2 * kCUs);
-    if (18 * big <= 11 * small) return launch_tiles<kMode, TO, 256, 256, 128, 64, 2>(a, stream);
+    if (kernel == kCarried) return launch_carried<kMode, TO, 128, 128, 64, 64>(a, stream);
+    if (kernel == kTiles256) return launch_tiles<kMode, TO, 256, 256, 128, 64, 2>(a, stream);
     return launch_tiles<kMode, TO, 128, 128, 64, 64, 2>(a, stream);
   } else {
-    return fed ? launch_exact<kMode, true, TO, 128, 128, 64, 64, 2>(a, stream)
-               : launch_exact<kMode, false, TO, 128, 128, 64, 64, 2>(a, stream);
+    if (kernel == kExactCarried) return launch_exact<kMode, false, TO, 128, 128, 64, 64, 2>(a, stream);
+    return launch_exact<kMode, true, TO, 128, 128, 64, 64, 2>(a, stream);
   }
 }
 
