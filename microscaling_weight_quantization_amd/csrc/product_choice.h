@@ -40,16 +40,23 @@ inline ProductKernel choose_kernel(Mode mode, bool fast, bool fed, int64_t I, in
     // The few-rows kernels read V anew for every 64 columns and U for every 64
     // rows, so they are the faster ones while they make about one workgroup for
     // each CU (192 rows x 4096 x 4096: 25.7 us against 29.3 in tiles; 192 x 8192 x
-    // 8192: 83.7 against 53.0), or, where 128 x 128 tiles fill the card, up to 8
-    // rows (y with FP8 sums: 5 rows each for 48 experts 19.4 against 21.5, 12 rows
-    // 26.1 against 23.6), none (dx: 1 row 18.9 against 13.7) or 32 (sums in fp32: 25
-    // rows 39 against 45, 40 rows 69 against 45).  Unaligned rows reach the tiles
-    // through registers, so the few-rows kernels hold out for twice as many.
+    // 8192: 83.7 against 53.0), and beyond for the fewest rows.  Where 128 x 128 tiles
+    // fill the card, those are up to 8 rows (y with FP8 sums: 5 rows each for 48 experts
+    // 19.4 against 21.5, 12 rows 26.1 against 23.6), none (dx: 1 row 18.9 against
+    // 13.7) or 32 (sums in fp32: 25 rows 39 against 45, 40 rows 69 against 45).  Where
+    // they do not, as when fewer rows than experts come, up to 8, none or 16 (18 rows
+    // for 48 experts of 1024 x 2048: 11.1 against 16.2, sums in fp32 12.2 against 22.0; 8
+    // rows x 20480 x 4096: 26.4 against 35.2; 32 rows of dx in fp32: 50 against 40).
+    // Unaligned rows reach the tiles through registers, so the few-rows kernels
+    // hold out for twice as many.
     const int64_t step = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     const int64_t groups = ((J + 63) / 64) * (experts ? experts * ((rows + step - 1) / step) : (rows + step - 1) / step);
     const bool full = tiles_of(I, J, experts, 128) >= kCUs * 3 / 4;
     const int64_t most = !fast ? 32 : mode == kForward ? 8 : 0;
-    if (!fed ? rows <= 16 || groups <= 2 * kCUs : full ? rows <= most : groups <= kCUs)
+    const bool few = !fed ? rows <= 16 || groups <= 2 * kCUs
+                   : full ? rows <= most
+                          : rows <= (most < 16 ? most : 16) || groups <= kCUs;
+    if (few)
       return step == 16 ? kFewRows16 : step == 32 ? kFewRows32 : kFewRows64;
   }
   if (!fast) return fed ? kExact : kExactCarried;

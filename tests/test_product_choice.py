@@ -59,3 +59,15 @@ def test_alignment_of_the_sizes():
     for c in CASES:
         axes = {"y": (c.R,), "dx": (c.R, c.J), "dw": (c.I, c.J)}[c.mode]
         assert not c.fed or all(a % 16 == 0 for a in axes), c
+
+
+def test_the_smallest_batches_take_the_few_rows_kernels(choose):
+    """One token by expert is fewer rows than experts: as many more tokens are, it is few rows."""
+    for experts, top_k, J in ((48, 6, 1024), (48, 6, 2048), (128, 8, 768), (8, 2, 14336)):
+        for mode, fast in (("y", True), ("y", False), ("dx", False)):
+            cases = [(mode, fast, True, t * top_k, J, experts) for t in (1, 2, 3, 4, 6, 9)]
+            assert set(choose(cases)) == {"kFewRows16"}, (experts, J, mode, fast)
+    # one weight: between the sizes whose few-rows workgroups fit the card and those whose tiles fill it
+    for J in (8192, 16384, 20480, 24576, 28672):
+        assert set(choose([("y", True, True, rows, J, 0) for rows in (1, 4, 8)])) == {"kFewRows16"}, J
+        assert set(choose([("y", False, True, rows, J, 0) for rows in (1, 4, 16)])) == {"kFewRows16"}, J
