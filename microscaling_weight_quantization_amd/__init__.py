@@ -1003,7 +1003,8 @@ def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: to
                               weights: Optional[torch.Tensor] = None, drows: Optional[torch.Tensor] = None,
                               dweights: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
     """Gradients of mxq_combine_rows for dy [tokens, H] -> (drows [rows, H], dweights fp32 [tokens, top_k]).
-    `position` names every row once, as mxq_sort_experts returns it."""
+    `position` names a row at most once, as mxq_sort_experts returns it.  Where `rows` has more of them than
+    there are slots, the gradient of the others is 0; a `drows` that is given keeps what it holds there."""
     L = _library(lib)
     pg, T0, H, ldg = _mat(dy)
     pr, R, hr, ldr = _mat(rows)
@@ -1011,6 +1012,8 @@ def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: to
     if (T0, hr) != (T, H) or dy.dtype != rows.dtype:
         raise ValueError(f"dy is [tokens, H] of the rows' dtype, got {dy.dtype} {list(dy.shape)} for "
                          f"{T} tokens and rows {rows.dtype} {list(rows.shape)}")
+    if drows is None and R > T * k:
+        drows = torch.zeros((R, H), dtype=rows.dtype, device=rows.device)
     drows, pd, ldd, _, dt = _result(dy, drows, (R, H), rows.dtype)
     if drows.dtype != rows.dtype:
         raise ValueError("drows must have the rows' dtype")
