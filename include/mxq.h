@@ -514,7 +514,9 @@ int mxq_quantize_fp8_group128_row_col(const void* x, int64_t ld_x, int64_t x_row
 /*
  * Products with 128x128 blockwise FP8 weights, on the matrix cores.  Operands are
  * E4M3 payloads with E8M0 codes as above; the sum over the reduction is held in
- * fp32, in a fixed order, and rounded once to the output's type (fast_accum below).
+ * fp32 and rounded once to the output's type (fast_accum below).  Its order is fixed by
+ * the sizes and alignment of the call: the same call gives the same bits, but a
+ * row's last places may differ between calls with other numbers of rows.
  *   mxq_matmul_fp8_block128        y[M, N]  = x[M, K] w[N, K]^T,  x's groups along K
  *   mxq_matmul_fp8_block128_dgrad  dx[M, K] = dy[M, N] w[N, K],   dy's groups along N
  *   mxq_matmul_fp8_group128_wgrad  dw[N, K] = dy[M, N]^T x[M, K], both in groups of

@@ -7,10 +7,12 @@
 // sort behind all others and are marked by the bitwise complement, which is
 // negative, in both directions (slots[] and position[]).
 //
-// The row kernels are bound by the bytes moved: 605 MB of sort and rows into order
-// take 155 us, 672 MB of rows back and their gradients 120 us (the second kernel
-// finds rows of the first in the last-level cache).  A few tokens' routing is two
-// launches and their calls on the host, 19.6 us.
+// The row kernels are bound by the bytes moved: sort and rows into order, 605 MB
+// with each row of x read once, take 155 us (a token's row passes the L2s for nearly
+// each of its 8 places: 510 MB read, largely from the last-level cache, and 537
+// written), 672 MB of rows back and their gradients 120 us (the second kernel finds
+// rows of the first in the last-level cache).  A few tokens' routing is two launches
+// and their calls on the host, 19.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -336,8 +338,10 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T* rows, int
 }
 
 // Gradients of combine: drows[p] = weight * dy[t], dweights[slot] = <dy[t], rows[p]>.
-// One workgroup per token, so dy is read once for all of the token's slots and
-// the dot products are summed in a fixed order.
+// One workgroup per token, so dy comes from memory once for all of the token's
+// slots (from the caches for those after the first) and the dot products are summed
+// in a fixed order.  Its 256 lanes take 2048 columns at a time; of narrower rows some
+// lanes have none.
 template <typename T, bool kVec, bool kStream>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(const T* dy, int64_t ld_dy, const T* rows,
                                                                        int64_t ld_rows, int n_rows,

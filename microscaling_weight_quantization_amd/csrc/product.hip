@@ -24,11 +24,12 @@
 //           through v_mfma_f32_32x32x16_bf16; with few rows a block is four
 //           v_mfma_f32_16x16x32_bf16, whose sum is scaled and added in fp32.
 //
-// Reached on one MI355X: 8192^3 with kFast 479 us (2290 TFLOP/s; a large library
-// product in FP8 reaches 2659), bound by the clock the card holds under this load;
-// dx of 1.9 TFLOP 832 us; dw of 103 GFLOP over experts with 480 MB of results 237 us
-// (its stores alone 81 us, the rest alone 170); one token through 235 MB of weights
-// 48.1 us (4.9 TB/s), bound by the weights' bytes.
+// Reached on one MI355X: 8192^3 with kFast 477 us (2304 TFLOP/s; a large library
+// product in FP8 reaches 2659), bound by the clock the card holds under this load (2.0
+// GHz of 2.4); dx of 1.9 TFLOP 832 us; dw of 103 GFLOP over experts with 403 MB of
+// results 239 us, bound by one workgroup a CU (294 registers a lane), which hides
+// neither a tile's start nor its stores; one token through 235 MB of weights 47.7 us
+// (4.9 TB/s where a plain read reaches 6.7): 448 workgroups on 256 CUs.
 //
 //   product   i   j   r    V                     U                     U's code
 //   y         m   n   k    x, r contiguous       w, r contiguous       (j / 128, r / 128)
@@ -1019,7 +1020,9 @@ bool feedable(const Operand& o, int contiguous, int64_t experts) {
 // reduction block of the same 16 kNJ rows of U, straight from memory to the
 // product instructions, one block ahead of them, and the waves' sums are added
 // through LDS in a fixed order at the end.  Where U's reduction axis is strided
-// (dx), a wave turns its block around in an LDS tile of its own.
+// (dx), a wave turns its block around in an LDS tile of its own.  The forms of eight
+// waves spill registers: 32 of y with 64 rows and sums in fp32, of dx with 64 rows 51 (FP8
+// sums, unaligned: none) and 78, of dx with 16 rows 21 and 22.
 
 // This lane's part of reduction r .. r + 127 of a row, which ends at r_end.
 template <bool kAligned>
