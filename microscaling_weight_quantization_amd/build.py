@@ -35,7 +35,7 @@ VARIANTS = {
     "libmxq_shapes.so": ["-O3"],
 }
 OBJECTS = ("group_quant", "product", "experts")
-OBJECT_HEADERS = ("checks.h", "segments.h", "fastdiv.h", "product_choice.h")
+OBJECT_HEADERS = ("checks.h", "segments.h", "fastdiv.h", "product_choice.h", "group128.h")
 SOURCES = {"libmxq_shapes.so": os.path.join(HERE, "csrc", "shapes.hip")}   # the others: SRC
 
 
