@@ -32,6 +32,12 @@
  *   mxq_matmul_fp8_group128_wgrad           dw = dy^T x
  *   mxq_sort_experts, mxq_sort_experts_workspace, mxq_dispatch_rows,
  *   mxq_combine_rows, mxq_combine_rows_backward
+ * and what stands between those products, each with its backward pass:
+ *   mxq_rms_norm, mxq_rms_norm_fp8_group128, mxq_rms_norm_fp8_group128_row_col,
+ *   mxq_rms_norm_backward           the norm before them, with the residual's addition
+ *   mxq_activate_fp8_group128, mxq_activate_fp8_group128_row_col,
+ *   mxq_activate_fp8_group128_backward      the (gated) activation between two of them
+ *   mxq_route_experts, mxq_route_experts_backward   tokens to experts, and their weights
  *
  * Sources, by page title and section:
  *   [QAT] "[PyTorch] MXFP4 weight QAT on MXFP8 and FP8 block-scaling recipes"
@@ -602,6 +608,130 @@ int mxq_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
                               const int32_t* position, const float* weights, int64_t n_tokens, int64_t top_k,
                               int64_t H, mxq_dtype dt, void* drows, int64_t ld_drows, float* dweights,
                               hipStream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it.
+ *   s = x + residual in fp32, rounded once to the residual's type (s = x without a
+ *   residual); y = s / sqrt(mean(s^2) + eps) * weight in fp32, rounded once to each output.
+ * The norm is that of s as it is stored, so that the backward pass, or the norm run
+ * again from a stored s, sees the same values.  A row's sum is in fp32 and its squares do not
+ * overflow.  A row that holds an Inf or NaN follows the formula: with a NaN all of it is NaN, with an
+ * Inf its finite elements are 0 and the others NaN.
+ *   x         [rows, K] of type dt, row stride ld_x >= K
+ *   residual  [rows, K] of type residual_dt; NULL: none, and residual_dt is not looked at
+ *   weight    [K] of type weight_dt, contiguous; NULL: all 1
+ *   eps       positive and finite (MXQ_ERR_SHAPE otherwise)
+ *   sum       [rows, K] of type residual_dt: s.  NULL: not wanted; MXQ_ERR_NULL where it is
+ *             wanted without a residual.  sum == residual with the same row stride (in place) is
+ *             allowed.
+ *   y         [rows, K] of type dt; NULL: not wanted (the FP8 forms only)
+ *   data, scale   y in FP8, groups of 128 along the row, as mxq_quantize_fp8_group128 lays
+ *             them out; quantized from y in fp32
+ * mxq_rms_norm_fp8_group128_row_col also writes groups of 128 rows of a column (as
+ * mxq_quantize_fp8_group128_col without experts).
+ *   workspace at least mxq_rms_norm_fp8_group128_row_col_workspace(rows) bytes, 8-byte
+ *             aligned, free again when the work is done
+ */
+int mxq_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, mxq_dtype residual_dt,
+                 const void* weight, mxq_dtype weight_dt, float eps, int64_t rows, int64_t K, mxq_dtype dt, void* sum,
+                 int64_t ld_sum, void* y, int64_t ld_y, hipStream_t stream);
+int mxq_rms_norm_fp8_group128(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                              mxq_dtype residual_dt, const void* weight, mxq_dtype weight_dt, float eps, int64_t rows,
+                              int64_t K, mxq_dtype dt, void* sum, int64_t ld_sum, void* y, int64_t ld_y, uint8_t* data,
+                              int64_t ld_data, uint8_t* scale, int64_t scale_ld, hipStream_t stream);
+int64_t mxq_rms_norm_fp8_group128_row_col_workspace(int64_t rows);
+int mxq_rms_norm_fp8_group128_row_col(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                                      mxq_dtype residual_dt, const void* weight, mxq_dtype weight_dt, float eps,
+                                      int64_t rows, int64_t K, mxq_dtype dt, void* sum, int64_t ld_sum, void* y,
+                                      int64_t ld_y, uint8_t* row_data, int64_t ld_row, uint8_t* row_scale,
+                                      int64_t row_scale_ld, uint8_t* col_data, int64_t ld_col, uint8_t* col_scale,
+                                      int64_t col_scale_ld, void* workspace, int64_t workspace_bytes,
+                                      hipStream_t stream);
+
+/*
+ * Gradients of the norm: with r = 1 / sqrt(mean(s^2) + eps), u = s r and g = dy w,
+ *   dx = r (g - u mean(g u)) + dresidual, the gradient of x and of the residual alike
+ *   dweight = sum over the rows of dy u, in fp32 and in an order that the sizes fix
+ *   dy         [rows, K] of type dt
+ *   x          [rows, K] of type x_dt: s, what was normalized (sum, or x without a residual)
+ *   dresidual  [rows, K] of type x_dt, the gradient that reaches s past the norm; NULL: none
+ *   dx         [rows, K] of type x_dt
+ *   dweight    [K] fp32; NULL: not wanted.  With no rows it is set to 0.
+ *   workspace  at least mxq_rms_norm_backward_workspace(rows, K) bytes, 16-byte aligned
+ */
+int64_t mxq_rms_norm_backward_workspace(int64_t rows, int64_t K);
+int mxq_rms_norm_backward(const void* dy, int64_t ld_dy, mxq_dtype dt, const void* x, int64_t ld_x, mxq_dtype x_dt,
+                          const void* weight, mxq_dtype weight_dt, float eps, const void* dresidual,
+                          int64_t ld_dresidual, int64_t rows, int64_t K, void* dx, int64_t ld_dx, float* dweight,
+                          void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* The activations: silu(g) = g / (1 + exp(-g)); gelu in its tanh form, g (1 + tanh(sqrt(2/pi)
+ * (g + 0.044715 g^3))) / 2; the squared relu, max(g, 0)^2. */
+typedef enum { MXQ_SILU = 0, MXQ_GELU_TANH = 1, MXQ_RELU2 = 2 } mxq_activation;
+
+/*
+ * The activation between the two products of a feed-forward layer, in FP8:
+ * a = act(gate) * up, or act(gate) where up is NULL; computed in fp32 and rounded once, to E4M3 in
+ * groups of 128 (codes and payloads as mxq_quantize_fp8_group128 gives them for a).
+ *   gate, up  [rows, F] bf16 or fp32, row strides ld_gate, ld_up >= F: the halves of an up
+ *             projection's result lie in one matrix of row stride 2 F
+ *   data      [rows, F], scale [rows, scale_ld >= ceil(F/128)]
+ * mxq_activate_fp8_group128_row_col: groups along the columns as well, begun anew with
+ * each expert's rows where offsets is given (see mxq_quantize_fp8_group128_col for the layout).
+ * mxq_activate_fp8_group128_backward: the gradients of both halves for da [rows, F],
+ *   dgate = da up act'(gate), dup = da act(gate), as one matrix [rows, 2 F] (dgate in its first F
+ *   columns; [rows, F] where up is NULL) in groups along rows and columns: the operands of the up
+ *   projection's own gradients.
+ * F is at most 2^29.
+ */
+int mxq_activate_fp8_group128(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int64_t rows, int64_t F,
+                              mxq_dtype dt, mxq_activation act, uint8_t* data, int64_t ld_data, uint8_t* scale,
+                              int64_t scale_ld, hipStream_t stream);
+int mxq_activate_fp8_group128_row_col(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int64_t rows,
+                                      int64_t F, mxq_dtype dt, mxq_activation act, const int32_t* offsets,
+                                      int64_t n_experts, uint8_t* row_data, int64_t ld_row, uint8_t* row_scale,
+                                      int64_t row_scale_ld, uint8_t* col_data, int64_t ld_col, uint8_t* col_scale,
+                                      int64_t col_scale_ld, hipStream_t stream);
+int mxq_activate_fp8_group128_backward(const void* da, int64_t ld_da, const void* gate, int64_t ld_gate, const void* up,
+                                       int64_t ld_up, int64_t rows, int64_t F, mxq_dtype dt, mxq_activation act,
+                                       const int32_t* offsets, int64_t n_experts, uint8_t* row_data, int64_t ld_row,
+                                       uint8_t* row_scale, int64_t row_scale_ld, uint8_t* col_data, int64_t ld_col,
+                                       uint8_t* col_scale, int64_t col_scale_ld, hipStream_t stream);
+
+/* How a router's logits become scores: softmax over the experts, or 1 / (1 + exp(-logit)) of each. */
+typedef enum { MXQ_SOFTMAX = 0, MXQ_SIGMOID = 1 } mxq_score;
+
+/*
+ * Each token's experts and their weights.  An expert's key is its logit, or with a bias
+ * score + bias, compared as 64 bits give it.  The top_k experts with the largest keys are chosen, in
+ * falling order; of equal keys the lower index comes first.
+ *   logits      [n_tokens, n_experts] bf16 or fp32, row stride ld_logits >= n_experts.  An expert
+ *               whose logit is -inf has score 0 and is closed to that token: never chosen.
+ *   bias        [n_experts] fp32, added to the scores for the choice alone (-inf closes an expert);
+ *               NULL: none
+ *   mask        [n_tokens] bytes; a token whose byte is 0 gets no experts.  NULL: all take part
+ *   n_groups, top_groups, group_top   the experts form n_groups groups of neighbours, as many in
+ *               each; only those of the top_groups best groups take part.  A group ranks by its largest
+ *               key (group_top 1) or by the sum of the scores, biased if there is a bias, of its two
+ *               experts with the largest keys (2; of one where no other is open); of equal groups
+ *               the lower index goes first.  n_groups 1: no such choice
+ *   ids         [n_tokens, top_k] int32, contiguous; -1 where no expert is left (such a slot is
+ *               dropped by mxq_sort_experts)
+ *   weights     [n_tokens, top_k] fp32: scale * score, or with renormalize scale * score / the sum
+ *               of the chosen scores; 0 for an id of -1
+ * A NaN key counts as the smallest of those that are open; weights of such a token may be NaN.
+ * 1 <= top_k <= top_groups * (n_experts / n_groups), n_experts <= 512, scale finite.
+ * mxq_route_experts_backward: the gradient of the logits for dweights [n_tokens, top_k], the
+ * choice held fixed (the bias has no gradient); slots whose id is not an expert's count nothing.
+ *   dlogits     [n_tokens, n_experts] of the logits' type, row stride ld_dlogits >= n_experts
+ */
+int mxq_route_experts(const void* logits, int64_t ld_logits, int64_t n_tokens, int64_t n_experts, mxq_dtype dt,
+                      const float* bias, const uint8_t* mask, mxq_score score, int renormalize, float scale,
+                      int64_t n_groups, int64_t top_groups, int64_t group_top, int64_t top_k, int32_t* ids,
+                      float* weights, hipStream_t stream);
+int mxq_route_experts_backward(const float* dweights, const void* logits, int64_t ld_logits, const int32_t* ids,
+                               int64_t n_tokens, int64_t n_experts, int64_t top_k, mxq_dtype dt, mxq_score score,
+                               int renormalize, float scale, void* dlogits, int64_t ld_dlogits, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -5,7 +5,8 @@ The ``mxq_*`` functions carry the names of the C entry points in
 row strides and sizes, and the call is enqueued on torch's current stream.
 Every step of the computation runs in the HIP kernels of ``csrc/`` (``mxq.hip``;
 ``group_quant.hip``, ``product.hip`` and ``experts.hip`` for the FP8 products, their
-operands and the experts' rows); there is no fallback of any kind, and a missing library raises.
+operands and the experts' rows; ``norm.hip``, ``activate.hip`` and ``route.hip`` for what stands
+between the products); there is no fallback of any kind, and a missing library raises.
 
 PyTorch is used for device memory and streams only.  A [rows, K] operand is a
 tensor whose last dimension is contiguous; leading dimensions of a contiguous
@@ -30,6 +31,8 @@ from . import build as _build
 MXQ_BF16, MXQ_FP32, MXQ_FP16 = 0, 1, 2
 MXQ_E4M3, MXQ_E5M2 = 0, 1
 MXQ_SCALE_ROW_1X32, MXQ_SCALE_TILE_128X128, MXQ_SCALE_COL_32X1 = 0, 1, 2
+MXQ_SILU, MXQ_GELU_TANH, MXQ_RELU2 = 0, 1, 2
+MXQ_SOFTMAX, MXQ_SIGMOID = 0, 1
 MXQ_OK, MXQ_ERR_NULL, MXQ_ERR_SHAPE, MXQ_ERR_DTYPE, MXQ_ERR_NO_ROWWISE_DATA, MXQ_ERR_ALIAS, MXQ_ERR_HIP = range(7)
 
 ENTRY_POINTS = ("mxq_status_string", "mxq_fake_quantize_mxfp4", "mxq_mxfp4_to_mxfp8_row",
@@ -43,7 +46,11 @@ ENTRY_POINTS = ("mxq_status_string", "mxq_fake_quantize_mxfp4", "mxq_mxfp4_to_mx
                 "mxq_quantize_fp8_group128", "mxq_quantize_fp8_group128_col", "mxq_quantize_fp8_group128_row_col",
                 "mxq_matmul_fp8_block128", "mxq_matmul_fp8_block128_dgrad", "mxq_matmul_fp8_group128_wgrad",
                 "mxq_sort_experts", "mxq_sort_experts_workspace", "mxq_dispatch_rows", "mxq_combine_rows",
-                "mxq_combine_rows_backward")
+                "mxq_combine_rows_backward", "mxq_rms_norm", "mxq_rms_norm_fp8_group128",
+                "mxq_rms_norm_fp8_group128_row_col_workspace", "mxq_rms_norm_fp8_group128_row_col",
+                "mxq_rms_norm_backward_workspace", "mxq_rms_norm_backward", "mxq_activate_fp8_group128",
+                "mxq_activate_fp8_group128_row_col", "mxq_activate_fp8_group128_backward", "mxq_route_experts",
+                "mxq_route_experts_backward")
 
 _libs = {}
 _lock = threading.Lock()
@@ -132,10 +139,28 @@ def load(name: str = "libmxq.so") -> ctypes.CDLL:
         L.mxq_dispatch_rows.argtypes = [vp, i64, i64, vp, i64, i64, i64, i32, vp, i64, vp]
         L.mxq_combine_rows.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64, vp]
         L.mxq_combine_rows_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64, vp, vp]
+        f32 = ctypes.c_float
+        norm = [vp, i64, vp, i64, i32, vp, i32, f32, i64, i64, i32, vp, i64, vp, i64]   # ... sum, ld_sum, y, ld_y
+        L.mxq_rms_norm.argtypes = norm + [vp]
+        L.mxq_rms_norm_fp8_group128.argtypes = norm + [u8p, i64] * 2 + [vp]
+        L.mxq_rms_norm_fp8_group128_row_col_workspace.argtypes = [i64]
+        L.mxq_rms_norm_fp8_group128_row_col.argtypes = norm + [u8p, i64] * 4 + [vp, i64, vp]
+        L.mxq_rms_norm_backward_workspace.argtypes = [i64, i64]
+        L.mxq_rms_norm_backward.argtypes = [vp, i64, i32, vp, i64, i32, vp, i32, f32, vp, i64, i64, i64, vp, i64, vp, vp,
+                                            i64, vp]
+        act = [vp, i64, vp, i64, i64, i64, i32, i32]                    # gate, ld, up, ld, rows, F, dtype, activation
+        L.mxq_activate_fp8_group128.argtypes = act + [u8p, i64] * 2 + [vp]
+        L.mxq_activate_fp8_group128_row_col.argtypes = act + [vp, i64] + [u8p, i64] * 4 + [vp]
+        L.mxq_activate_fp8_group128_backward.argtypes = [vp, i64] + act + [vp, i64] + [u8p, i64] * 4 + [vp]
+        L.mxq_route_experts.argtypes = [vp, i64, i64, i64, i32, vp, vp, i32, i32, f32, i64, i64, i64, i64, vp, vp, vp]
+        L.mxq_route_experts_backward.argtypes = [vp, vp, i64, vp, i64, i64, i64, i32, i32, i32, f32, vp, i64, vp]
         for n in ENTRY_POINTS[1:]:
             getattr(L, n).restype = i64 if n.endswith("_workspace") else i32
         _libs[name] = L
         return L
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device_operands(fn):
@@ -154,6 +179,9 @@ def _device_operands(fn):
                     dev = d
                 elif d != dev:
                     raise ValueError(f"{fn.__name__}: operands on cuda:{dev} and cuda:{d}; all must be on one device")
+        if dev >= 0 and dev != _current_device():   # a launch goes to the current device
+            with torch.cuda.device(dev):
+                return fn(*args, **kwargs)
         return fn(*args, **kwargs)
     return wrapper
 
@@ -1022,6 +1050,270 @@ def mxq_combine_rows_backward(dy: torch.Tensor, rows: torch.Tensor, position: to
     pv = _vector(dweights, T * k, torch.float32, "dweights")
     _check(L, L.mxq_combine_rows_backward(pg, ldg, pr, ldr, R, pp, pw, T, k, H, dt, pd, ldd, pv, _handle(dy)))
     return drows, dweights
+
+
+# ---- between the FP8 products: norm, activation, routing -----------------------------------
+
+def _weight_of(weight: Optional[torch.Tensor], K: int):
+    """(pointer, dtype code) of a norm's weight."""
+    if weight is None:
+        return None, MXQ_FP32
+    if weight.shape != (K,) or not weight.is_contiguous():
+        raise ValueError(f"weight is a contiguous tensor of {K} elements, got {list(weight.shape)}")
+    return weight.data_ptr(), _float_code(weight)
+
+
+def _same_rows(t: torch.Tensor, rows: int, cols: int, what: str):
+    """(pointer, row stride) of an input [rows, cols], no more and no less."""
+    p, r, c, ld = _mat(t)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{what} is [{rows}, {cols}], got {list(t.shape)}")
+    return p, ld
+
+
+def _float_out(like: torch.Tensor, out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, what: str):
+    """(tensor, pointer, row stride) of a floating output shaped as `like`, allocated if missing."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=dtype, device=like.device)
+        return out, out.data_ptr(), cols
+    if out.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {out.dtype}")
+    return (out, *_same_rows(out, rows, cols, what))
+
+
+def _norm_operands(x, weight, eps, residual, residual_out, y, with_y):
+    """The norm's leading arguments, rows, K, and its floating outputs (s or None, y or None)."""
+    px, rows, K, ldx = _mat(x)
+    pw, wdt = _weight_of(weight, K)
+    dt = _float_code(x)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        pr, ldr, rdt, s, ps, lds = None, 0, dt, None, None, 0
+    else:
+        rdt = _float_code(residual)
+        pr, ldr = _same_rows(residual, rows, K, "residual")
+        s, ps, lds = _float_out(x, residual_out, rows, K, residual.dtype, "residual_out")
+    py, ldy = None, 0
+    if y is not None or with_y:
+        y, py, ldy = _float_out(x, y, rows, K, x.dtype, "y")
+    return (px, ldx, pr, ldr, rdt, pw, wdt, eps, rows, K, dt, ps, lds, py, ldy), rows, K, s, y
+
+
+@_device_operands
+def mxq_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """y = s / sqrt(mean(s^2) + eps) * weight over each row of s = x + residual (bf16 / fp32), s rounded
+    to the residual's type -> (y of x's type, s).  s goes to `residual_out`, which may be `residual`
+    itself; without a residual s is x and None comes back for it.  `weight` [K] bf16 / fp32, None: all 1."""
+    L = _library(lib)
+    args, _, _, s, y = _norm_operands(x, weight, eps, residual, residual_out, y, True)
+    _check(L, L.mxq_rms_norm(*args, _handle(x)))
+    return y, s
+
+
+@_device_operands
+def mxq_rms_norm_fp8_group128(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                              residual: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+                              y: Optional[torch.Tensor] = None, with_y: bool = False,
+                              data: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                              lib: str = "libmxq.so"):
+    """The norm in FP8, groups of 128 along the rows -> (payload uint8 [rows, K], codes uint8
+    [rows, ceil(K/128)], s, y).  s as mxq_rms_norm returns it; y None unless `with_y` or a tensor for it."""
+    L = _library(lib)
+    args, rows, K, s, y = _norm_operands(x, weight, eps, residual, residual_out, y, with_y)
+    data, pd, ldd = _bytes_for(x, data, rows, K, "payload")
+    scale, pc, ldc = _bytes_for(x, scale, rows, _ng(K), "scale")
+    _check(L, L.mxq_rms_norm_fp8_group128(*args, pd, ldd, pc, ldc, _handle(x)))
+    return data, scale, s, y
+
+
+@_device_operands
+def mxq_rms_norm_fp8_group128_row_col(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                                      residual: Optional[torch.Tensor] = None,
+                                      residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                                      with_y: bool = False, row_data: Optional[torch.Tensor] = None,
+                                      row_scale: Optional[torch.Tensor] = None, col_data: Optional[torch.Tensor] = None,
+                                      col_scale: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """The norm in FP8, groups of 128 along the rows and along the columns (the operand of a weight
+    gradient) -> (row payload, row codes, column payload, column codes, s, y)."""
+    L = _library(lib)
+    args, rows, K, s, y = _norm_operands(x, weight, eps, residual, residual_out, y, with_y)
+    row_data, prd, ldrd = _bytes_for(x, row_data, rows, K, "row payload")
+    row_scale, prs, ldrs = _bytes_for(x, row_scale, rows, _ng(K), "row_scale")
+    col_data, pcd, ldcd = _bytes_for(x, col_data, rows, K, "column payload")
+    col_scale, pcs, ldcs = _bytes_for(x, col_scale, _ng(rows), K, "col_scale")
+    need = L.mxq_rms_norm_fp8_group128_row_col_workspace(rows)
+    ws = torch.empty(need, dtype=_UINT8, device=x.device)
+    _check(L, L.mxq_rms_norm_fp8_group128_row_col(*args, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs, ws.data_ptr(), need,
+                                                  _handle(x)))
+    return row_data, row_scale, col_data, col_scale, s, y
+
+
+@_device_operands
+def mxq_rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e-6,
+                          dresidual: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                          dweight: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """Gradients of the norm for dy -> (dx of x's type, dweight fp32 [K]).  `x` is what was normalized: s where
+    there was a residual.  `dresidual` (x's type) is the gradient that reaches s past the norm; dx holds
+    both, the gradient of the norm's x and of its residual alike."""
+    L = _library(lib)
+    px, rows, K, ldx = _mat(x)
+    pg, ldg = _same_rows(dy, rows, K, "dy")
+    pw, wdt = _weight_of(weight, K)
+    pr, ldr = None, 0
+    if dresidual is not None:
+        if dresidual.dtype != x.dtype:
+            raise ValueError(f"dresidual must be {x.dtype}, got {dresidual.dtype}")
+        pr, ldr = _same_rows(dresidual, rows, K, "dresidual")
+    dx, pd, ldd = _float_out(x, dx, rows, K, x.dtype, "dx")
+    if dweight is None:
+        dweight = torch.empty(K, dtype=_FLOAT32, device=x.device)
+    pv = _vector(dweight, K, _FLOAT32, "dweight")
+    need = L.mxq_rms_norm_backward_workspace(rows, K)
+    ws = torch.empty(need, dtype=_UINT8, device=x.device)
+    _check(L, L.mxq_rms_norm_backward(pg, ldg, _float_code(dy), px, ldx, _float_code(x), pw, wdt, eps, pr, ldr, rows, K,
+                                      pd, ldd, pv, ws.data_ptr(), need, _handle(x)))
+    return dx, dweight
+
+
+_ACTIVATIONS = {"silu": MXQ_SILU, "gelu_tanh": MXQ_GELU_TANH, "relu2": MXQ_RELU2}
+_SCORES = {"softmax": MXQ_SOFTMAX, "sigmoid": MXQ_SIGMOID}
+
+
+def _named(names: dict, name: str, what: str) -> int:
+    if name not in names:
+        raise ValueError(f"{what} is one of {', '.join(names)}, got {name!r}")
+    return names[name]
+
+
+def _halves(gate: torch.Tensor, up: Optional[torch.Tensor], activation: str):
+    """The activation's leading arguments, rows and F."""
+    pg, rows, F, ldg = _mat(gate)
+    pu, ldu = None, 0
+    if up is not None:
+        if up.dtype != gate.dtype:
+            raise ValueError(f"gate and up must have one dtype, got {gate.dtype} and {up.dtype}")
+        pu, ldu = _same_rows(up, rows, F, "up")
+    return (pg, ldg, pu, ldu, rows, F, _float_code(gate), _named(_ACTIVATIONS, activation, "activation")), rows, F
+
+
+@_device_operands
+def mxq_activate_fp8_group128(gate: torch.Tensor, up: Optional[torch.Tensor] = None, activation: str = "silu",
+                              data: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                              lib: str = "libmxq.so"):
+    """act(gate) * up (bf16 / fp32 [rows, F], `up` None: act(gate)) in FP8, groups of 128 along the rows ->
+    (payload uint8 [rows, F], codes uint8 [rows, ceil(F/128)]).  `activation`: "silu", "gelu_tanh" or "relu2"
+    (the squared relu).  gate and up may be the halves of one matrix: h[:, :F], h[:, F:]."""
+    L = _library(lib)
+    args, rows, F = _halves(gate, up, activation)
+    data, pd, ldd = _bytes_for(gate, data, rows, F, "payload")
+    scale, ps, lds = _bytes_for(gate, scale, rows, _ng(F), "scale")
+    _check(L, L.mxq_activate_fp8_group128(*args, pd, ldd, ps, lds, _handle(gate)))
+    return data, scale
+
+
+@_device_operands
+def mxq_activate_fp8_group128_row_col(gate: torch.Tensor, up: Optional[torch.Tensor] = None, activation: str = "silu",
+                                      offsets: Optional[torch.Tensor] = None,
+                                      row_data: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None,
+                                      col_data: Optional[torch.Tensor] = None, col_scale: Optional[torch.Tensor] = None,
+                                      lib: str = "libmxq.so"):
+    """The same with groups of 128 along the rows and along the columns, these begun anew with each expert's rows
+    where `offsets` is given -> (row payload, row codes, column payload, column codes)."""
+    L = _library(lib)
+    args, rows, F = _halves(gate, up, activation)
+    po, n = (None, 0) if offsets is None else _experts_of(offsets)
+    row_data, prd, ldrd = _bytes_for(gate, row_data, rows, F, "row payload")
+    row_scale, prs, ldrs = _bytes_for(gate, row_scale, rows, _ng(F), "row_scale")
+    col_data, pcd, ldcd = _bytes_for(gate, col_data, rows, F, "column payload")
+    col_scale, pcs, ldcs = _bytes_for(gate, col_scale, _code_rows(rows, n), F, "col_scale")
+    _check(L, L.mxq_activate_fp8_group128_row_col(*args, po, n, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs,
+                                                  _handle(gate)))
+    return row_data, row_scale, col_data, col_scale
+
+
+@_device_operands
+def mxq_activate_fp8_group128_backward(da: torch.Tensor, gate: torch.Tensor, up: Optional[torch.Tensor] = None,
+                                       activation: str = "silu", offsets: Optional[torch.Tensor] = None,
+                                       row_data: Optional[torch.Tensor] = None,
+                                       row_scale: Optional[torch.Tensor] = None,
+                                       col_data: Optional[torch.Tensor] = None,
+                                       col_scale: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """Gradients of gate and up for da [rows, F], side by side as one [rows, 2 F] ([rows, F] without `up`) in FP8
+    with groups of 128 along the rows and along the columns: what the up projection's input and weight
+    gradients take -> (row payload, row codes, column payload, column codes)."""
+    L = _library(lib)
+    args, rows, F = _halves(gate, up, activation)
+    if da.dtype != gate.dtype:
+        raise ValueError(f"da and gate must have one dtype, got {da.dtype} and {gate.dtype}")
+    pa, lda = _same_rows(da, rows, F, "da")
+    po, n = (None, 0) if offsets is None else _experts_of(offsets)
+    K = F if up is None else 2 * F
+    row_data, prd, ldrd = _bytes_for(gate, row_data, rows, K, "row payload")
+    row_scale, prs, ldrs = _bytes_for(gate, row_scale, rows, _ng(K), "row_scale")
+    col_data, pcd, ldcd = _bytes_for(gate, col_data, rows, K, "column payload")
+    col_scale, pcs, ldcs = _bytes_for(gate, col_scale, _code_rows(rows, n), K, "col_scale")
+    _check(L, L.mxq_activate_fp8_group128_backward(pa, lda, *args, po, n, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs,
+                                                   _handle(gate)))
+    return row_data, row_scale, col_data, col_scale
+
+
+def _logits_of(logits: torch.Tensor):
+    if logits.dim() != 2:
+        raise ValueError(f"logits is [tokens, experts], got {list(logits.shape)}")
+    return _mat(logits)
+
+
+@_device_operands
+def mxq_route_experts(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+                      renormalize: bool = True, scale: float = 1.0, n_groups: int = 1, top_groups: int = 1,
+                      group_top: int = 1, mask: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+                      weights: Optional[torch.Tensor] = None, lib: str = "libmxq.so"):
+    """Each token's experts and their weights from a router's logits (bf16 / fp32 [tokens, experts]) ->
+    (ids int32 [tokens, top_k], weights fp32 [tokens, top_k]), the operands of mxq_sort_experts and
+    mxq_combine_rows.  `score` "softmax" or "sigmoid"; `bias` fp32 [experts] is added to the scores for the choice
+    alone; with `n_groups` > 1 only the experts of the `top_groups` best groups take part, a group ranked by
+    its largest key (`group_top` 1) or by the sum of its two best (2).  The chosen scores are the weights,
+    made to sum to 1 with `renormalize`, times `scale`.  An expert whose logit is -inf is closed;
+    a token whose `mask` (bool [tokens]) is False has none.  Slots that no expert is left for hold -1 and 0."""
+    L = _library(lib)
+    pl, T, E, ldl = _logits_of(logits)
+    pb = None if bias is None else _vector(bias, E, _FLOAT32, "bias")
+    pm = None
+    if mask is not None:
+        if mask.dtype not in (torch.bool, _UINT8) or mask.numel() != T or not mask.is_contiguous():
+            raise ValueError(f"mask is a contiguous bool tensor of {T} elements, got {mask.dtype} {list(mask.shape)}")
+        pm = mask.data_ptr()
+    if top_k < 1:
+        raise ValueError(f"top_k is at least 1, got {top_k}")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=_INT32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=_FLOAT32, device=logits.device)
+    pi, pw = _vector(ids, T * top_k, _INT32, "ids"), _vector(weights, T * top_k, _FLOAT32, "weights")
+    _check(L, L.mxq_route_experts(pl, ldl, T, E, _float_code(logits), pb, pm, _named(_SCORES, score, "score"), renormalize,
+                                  scale, n_groups, top_groups, group_top, top_k, pi, pw, _handle(logits)))
+    return ids, weights
+
+
+@_device_operands
+def mxq_route_experts_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                               renormalize: bool = True, scale: float = 1.0, dlogits: Optional[torch.Tensor] = None,
+                               lib: str = "libmxq.so") -> torch.Tensor:
+    """Gradient of mxq_route_experts' logits for that of its weights, the choice `ids` held fixed ->
+    [tokens, experts] of the logits' type.  `score`, `renormalize` and `scale` as in the forward call."""
+    L = _library(lib)
+    pl, T, E, ldl = _logits_of(logits)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids is int32 [{T}, top_k], got {list(ids.shape)}")
+    top_k = ids.shape[1]
+    pi, pg = _vector(ids, T * top_k, _INT32, "ids"), _vector(dweights, T * top_k, _FLOAT32, "dweights")
+    dlogits, pd, ldd = _float_out(logits, dlogits, T, E, logits.dtype, "dlogits")
+    _check(L, L.mxq_route_experts_backward(pg, pl, ldl, pi, T, E, top_k, _float_code(logits),
+                                           _named(_SCORES, score, "score"), renormalize, scale, pd, ldd, _handle(logits)))
+    return dlogits
 
 
 # ---- convenience layer ------------------------------------------------------------------

@@ -5,8 +5,8 @@
 the build-variant tests: ``libmxq_fastmath.so`` (fast-math, denormals flushed),
 ``libmxq_o1.so`` (-O1) and ``libmxq_o0.so`` (-O0, no optimisation).  Every
 step of the path is integer arithmetic, so all four builds must produce
-identical bits.  The FP8 products, their quantizer and the expert routing
-(``OBJECTS``) are compiled once, with -O3, and linked into all four.
+identical bits.  The FP8 products, their quantizer, the expert routing and what
+stands between the products (``OBJECTS``) are compiled once, with -O3, and linked into all four.
 ``libmxq_shapes.so`` holds the access-shape reference kernels
 (``csrc/shapes.hip``) that bench.py times beside the library's kernels.
 """
@@ -34,8 +34,9 @@ VARIANTS = {
     "libmxq_o0.so": ["-O0"],
     "libmxq_shapes.so": ["-O3"],
 }
-OBJECTS = ("group_quant", "product", "experts")
-OBJECT_HEADERS = ("checks.h", "segments.h", "fastdiv.h", "product_choice.h", "group128.h")
+OBJECTS = ("group_quant", "product", "experts", "norm", "activate", "route")
+OBJECT_HEADERS = ("checks.h", "segments.h", "fastdiv.h", "product_choice.h", "group128.h",
+                  "floats.h")
 SOURCES = {"libmxq_shapes.so": os.path.join(HERE, "csrc", "shapes.hip")}   # the others: SRC
 
 

@@ -1,5 +1,6 @@
-// Host-side argument checks of the FP8 group quantizer, the FP8 products and the
-// expert routing (group_quant.hip, product.hip, experts.hip): byte ranges of the
+// Host-side argument checks of the FP8 group quantizer, the FP8 products, the expert
+// routing and what stands between them (group_quant.hip, product.hip, experts.hip,
+// norm.hip, activate.hip, route.hip): byte ranges of the
 // operands, overlap, alignment, launch status.  mxq.hip has the same rules in
 // its own words, for its own list-of-weights calls.
 #pragma once
@@ -69,6 +70,12 @@ inline int64_t rows_per_launch(int64_t lanes) { return ((int64_t)1 << 31) / lane
 inline bool is_float(mxq_dtype dt) { return dt == MXQ_BF16 || dt == MXQ_FP32; }
 inline size_t size_of(mxq_dtype dt) { return dt == MXQ_BF16 ? 2 : 4; }
 inline int64_t groups_of(int64_t n) { return (n + 127) / 128; }
+
+// Whether rows can be read or written 16 bytes at a time, and payloads 8.  An operand that is not there can.
+inline bool wide_rows(const void* p, int64_t ld, mxq_dtype dt) {
+  return !p || (aligned(p, 16) && ld % (16 / (int64_t)size_of(dt)) == 0);
+}
+inline bool wide_payload(const uint8_t* p, int64_t ld) { return !p || (aligned(p, 8) && ld % 8 == 0); }
 
 // Rows, columns and slots are counted in 32 bits on the device.
 constexpr int64_t kMaxDim = (int64_t)1 << 30;

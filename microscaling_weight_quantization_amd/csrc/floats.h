@@ -1,0 +1,91 @@
+// Eight elements of a row as floats, rounded once on their way out, and sums over a
+// row's lanes (norm.hip, activate.hip, route.hip).
+#pragma once
+
+#include "group128.h"
+
+namespace mxq_dev {
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// The types as the kernels name them: uint16_t for bf16, uint32_t for fp32 bit patterns.
+template <typename T>
+__device__ __forceinline__ f32x8 widen(const Chunk<T>& v) {
+  f32x8 f;
+#pragma unroll
+  for (int i = 0; i < kEPL; i++) {
+    if constexpr (sizeof(T) == 2)
+      f[i] = __builtin_bit_cast(float, i & 1 ? v.w[i / 2] & 0xFFFF0000u : v.w[i / 2] << 16);
+    else
+      f[i] = __builtin_bit_cast(float, v.w[i]);
+  }
+  return f;
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> narrow(f32x8 f) {
+  Chunk<T> v;
+  if constexpr (sizeof(T) == 2) {
+    const bf16x8 b = __builtin_convertvector(f, bf16x8);   // to nearest, ties to even
+#pragma unroll
+    for (int i = 0; i < 4; i++) v.w[i] = __builtin_bit_cast(u32x4, b)[i];
+  } else {
+    const u32x8 b = __builtin_bit_cast(u32x8, f);   // as a whole: of one element the cast takes the vector's first
+#pragma unroll
+    for (int i = 0; i < kEPL; i++) v.w[i] = b[i];
+  }
+  return v;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ f32x8 load_floats(const void* row, int c, int K) {
+  return widen<T>(load_chunk<T, kVec>((const T*)row, c, K));
+}
+
+template <typename T, bool kVec, bool kStream = false>
+__device__ __forceinline__ void store_floats(void* row, int c, int K, f32x8 f) {
+  const Chunk<T> v = narrow<T>(f);
+  T* const p = (T*)row + c;
+  if (kVec) {
+    if (c < K) {
+#pragma unroll
+      for (int i = 0; i < Chunk<T>::kWords / 4; i++) {
+        const u32x4 q{v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]};
+        if (kStream) __builtin_nontemporal_store(q, (u32x4*)p + i);
+        else ((u32x4*)p)[i] = q;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEPL; i++)
+      if (c + i < K) {
+        if constexpr (sizeof(T) == 2) p[i] = (T)(v.w[i / 2] >> (16 * (i & 1)));
+        else p[i] = v.w[i];
+      }
+  }
+}
+
+// Payload and code of the group of a row that 16 lanes hold, eight values each.
+template <bool kVec, bool kStream>
+__device__ __forceinline__ void store_group(uint8_t* data, uint8_t* scale, int c, int K, f32x8 f) {
+  const Chunk<uint32_t> v = narrow<uint32_t>(f);
+  const uint32_t code = code_of<uint32_t>(max16(v.amax()));
+  store_chunk<kVec, kStream>(data, c, K, payload_of(v, code));
+  if ((threadIdx.x & 15) == 0 && c < K) scale[c / kGroup] = (uint8_t)code;
+}
+
+__device__ __forceinline__ float add8(f32x8 v) {
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+// Sum over the aligned groups of kLanes lanes of a wave, the same in each of them.
+template <int kLanes>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < kLanes; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+}  // namespace mxq_dev
