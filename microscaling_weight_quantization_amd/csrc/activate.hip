@@ -27,78 +27,106 @@ struct ActArgs {
   int act;
 };
 
-// p(z), and 1 - p(z), without overflow and without cancellation in either tail.
-struct Logistic {
-  float p, q;
-};
-__device__ __forceinline__ Logistic logistic(float z) {
-  const float e = exp2f(-fabsf(z) * 1.44269504088896341f);
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return z < 0 ? Logistic{e * r, r} : Logistic{r, e * r};
+// p(z) without overflow and without loss where z is far below 0: with t = 2^64 exp(-|z|) it is t / (1 + exp(-|z|)) or
+// 2^64 / (1 + exp(-|z|)), times 2^-64; t stays a normal number down to exp(-|z|) = 2^-190.
+__device__ __forceinline__ float logistic(float z) {
+  const float t = __builtin_amdgcn_exp2f(fmaf(-fabsf(z), 1.44269504088896341f, 64.0f));
+  const float r = __builtin_amdgcn_rcpf(fmaf(t, 0x1p-64f, 1.0f));
+  return (z < 0 ? t : 0x1p64f) * r * 0x1p-64f;
 }
 
 constexpr float kGelu = 1.59576912160573071f;   // 2 sqrt(2 / pi)
 constexpr float kCube = 0.044715f;
 
-__device__ __forceinline__ f32x8 act_of(int act, f32x8 g) {
-  f32x8 a;
-  if (act == MXQ_SILU) {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) a[i] = g[i] * logistic(g[i]).p;
-  } else if (act == MXQ_GELU_TANH) {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) a[i] = g[i] * logistic(kGelu * (g[i] + kCube * g[i] * g[i] * g[i])).p;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) a[i] = g[i] > 0 ? g[i] * g[i] : (g[i] <= 0 ? 0.0f : g[i]);   // a NaN stays one
-  }
-  return a;
+// max(g, 0), a NaN if g is one.
+__device__ __forceinline__ float positive(float g) { return __builtin_elementwise_maximum(g, 0.0f); }
+
+template <int kAct>
+__device__ __forceinline__ float act_of(float g) {
+  if constexpr (kAct == MXQ_SILU) return g * logistic(g);
+  if constexpr (kAct == MXQ_GELU_TANH) return g * logistic(kGelu * (g + kCube * g * g * g));
+  return positive(g) * positive(g);
 }
 
 // act(g) into *a, act'(g) as the result.
-__device__ __forceinline__ f32x8 slope_of(int act, f32x8 g, f32x8* a) {
-  f32x8 d;
-  if (act == MXQ_SILU) {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) {
-      const Logistic l = logistic(g[i]);
-      (*a)[i] = g[i] * l.p;
-      d[i] = l.p * (1.0f + g[i] * l.q);
-    }
-  } else if (act == MXQ_GELU_TANH) {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) {
-      const float g2 = g[i] * g[i];
-      const Logistic l = logistic(kGelu * g[i] * (1.0f + kCube * g2));
-      (*a)[i] = g[i] * l.p;
-      // far out q is 0 and g may be anything: the product is then 0, not 0 * Inf
-      const float t = l.p * l.q;
-      d[i] = l.p + (t == 0.0f ? 0.0f : g[i] * t * kGelu * (1.0f + 3.0f * kCube * g2));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEPL; i++) {
-      const float r = g[i] > 0 ? g[i] : (g[i] <= 0 ? 0.0f : g[i]);
-      (*a)[i] = r * r;
-      d[i] = 2.0f * r;
-    }
+template <int kAct>
+__device__ __forceinline__ float slope_of(float g, float* a) {
+  if constexpr (kAct == MXQ_SILU) {
+    const float p = logistic(g);
+    *a = g * p;
+    return p + *a * (1.0f - p);
   }
-  return d;
+  if constexpr (kAct == MXQ_GELU_TANH) {
+    const float g2 = g * g;
+    const float p = logistic(kGelu * g * (1.0f + kCube * g2));
+    *a = g * p;
+    // far out p (1 - p) is 0 and g may be anything: the product is then 0, not 0 * Inf
+    const float t = *a * (1.0f - p);
+    return p + (t == 0.0f ? 0.0f : t * kGelu * (1.0f + 3.0f * kCube * g2));
+  }
+  const float r = positive(g);
+  *a = r * r;
+  return 2.0f * r;
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ f32x8 value_at(const ActArgs& s, int64_t r, int c) {
-  const f32x8 g = load_floats<T, kVec>((const T*)s.gate + r * s.ld_gate, c, s.F);
-  f32x8 a = act_of(s.act, g);
-  if (s.up) a *= load_floats<T, kVec>((const T*)s.up + r * s.ld_up, c, s.F);
-  return a;
+// What a lane reads for eight elements of a row; da in the backward pass only.
+template <typename T, bool kBack>
+struct Raw {
+  Chunk<T> gate, up, da;
+};
+// kOnce: each line is read by one instruction and by no other workgroup, and leaves with the non-temporal hint.  That holds
+// for bf16 (a lane's 32 bytes of fp32 are two loads, each of half of every line): 49152 x 1024 bf16 forward 55.9 -> 54.1 us,
+// backward 106.3 -> 94.2; 16000 x 1024 fp32 29.9 -> 34.2 and 51.6 -> 55.6, so not there; and 16000 x 1000 bf16 backward,
+// where two workgroups read each line, 53.5 -> 60.5.
+template <typename T, bool kVec, bool kOnce, bool kBack>
+__device__ __forceinline__ void load_raw(Raw<T, kBack>& v, const ActArgs& s, int64_t r, int c) {
+  v.gate = load_chunk<T, kVec, kOnce>((const T*)s.gate + r * s.ld_gate, c, s.F);
+  if (s.up) v.up = load_chunk<T, kVec, kOnce>((const T*)s.up + r * s.ld_up, c, s.F);
+  if constexpr (kBack) v.da = load_chunk<T, kVec, kOnce>((const T*)s.da + r * s.ld_da, c, s.F);
+}
+
+// The rows of a tile of which this lane holds every kStep-th, one after the other.
+template <typename T, bool kVec, bool kOnce, bool kBack, bool kWhole, int kStep>
+struct Walk {
+  const ActArgs& s;
+  const T *gate, *up, *da;
+  int row, have, c;
+  int64_t first;
+  __device__ __forceinline__ Walk(const ActArgs& a, const TileRows& t, int column)
+      : s(a), row(threadIdx.x / 16), have(t.have()), c(column + (threadIdx.x & 15) * kEPL), first(t.first) {
+    if constexpr (kWhole) {
+      gate = (const T*)s.gate + first * s.ld_gate + row * s.ld_gate + c;
+      up = s.up ? (const T*)s.up + first * s.ld_up + row * s.ld_up + c : nullptr;
+      if constexpr (kBack) da = (const T*)s.da + first * s.ld_da + row * s.ld_da + c;
+    }
+  }
+  __device__ __forceinline__ void next(Raw<T, kBack>& v) {
+    if constexpr (kWhole) {
+      v.gate = load_chunk<T, kVec, kOnce>(gate, 0, 1);
+      gate += kStep * s.ld_gate;
+      if (s.up) v.up = load_chunk<T, kVec, kOnce>(up, 0, 1), up += kStep * s.ld_up;
+      if constexpr (kBack) v.da = load_chunk<T, kVec, kOnce>(da, 0, 1), da += kStep * s.ld_da;
+    } else {
+      load_raw<T, kVec, kOnce>(v, s, first + min(row, have - 1), row < have ? c : s.F);
+      row += kStep;
+    }
+  }
+};
+
+template <typename T, int kAct>
+__device__ __forceinline__ f32x8 value_of(const Raw<T, false>& v, bool gated) {
+  const f32x8 g = widen<T>(v.gate);
+  f32x8 a;
+#pragma unroll
+  for (int i = 0; i < kEPL; i++) a[i] = act_of<kAct>(g[i]);
+  return gated ? a * widen<T>(v.up) : a;
 }
 
 // ---- groups along the rows ------------------------------------------------------------
 // 16 lanes per group, 16 groups per workgroup, one group a lane.
 constexpr int kRowThreads = 256;
 
-template <typename T, bool kVec>
+template <typename T, int kAct, bool kVec>
 __global__ __launch_bounds__(kRowThreads) void act_rows_kernel(ActArgs s, MxqDivisor groups, uint32_t total,
                                                                uint8_t* data, int64_t ld_data, uint8_t* scale,
                                                                int64_t scale_ld) {
@@ -107,93 +135,151 @@ __global__ __launch_bounds__(kRowThreads) void act_rows_kernel(ActArgs s, MxqDiv
   if (g >= total) return;   // whole groups of 16 lanes leave together
   const uint32_t r = mxq_quot(g, groups), b = g - r * groups.d;
   const int c = (int)b * kGroup + (threadIdx.x & 15) * kEPL;
-  const f32x8 a = value_at<T, kVec>(s, r, c);
-  store_group<kVec, false>(data + (int64_t)r * ld_data, scale + (int64_t)r * scale_ld, c, s.F, a);
+  Raw<T, false> v;
+  load_raw<T, kVec, false>(v, s, r, c);
+  store_group<kVec, false>(data + (int64_t)r * ld_data, scale + (int64_t)r * scale_ld, c, s.F,
+                           value_of<T, kAct>(v, s.up != nullptr));
 }
 
 // ---- groups along both -----------------------------------------------------------------
-template <typename T, bool kVec, bool kStream>
-__global__ __launch_bounds__(kTileThreads) void act_tiles_kernel(ActArgs s, int first_id, int rows,
-                                                                 const int32_t* offsets, int experts, TileOut out) {
+template <typename T, int kAct, bool kVec, bool kWhole, int kRows>
+__device__ __forceinline__ void act_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
+                                         TileShared<kRows>& shared) {
+  Chunk<uint32_t> v[kRows];
+  constexpr int kAtOnce = sizeof(T) == 2 ? kRows : kRows / 2;   // rows whose operands are on their way at once
+  Walk<T, kVec, kVec && sizeof(T) == 2, false, kWhole, kGroup / kRows> walk(s, t, blockIdx.x * kGroup);
+#pragma unroll
+  for (int i0 = 0; i0 < kRows; i0 += kAtOnce) {
+    Raw<T, false> raw[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; i++) walk.next(raw[i]);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; i++) v[i0 + i] = narrow<uint32_t>(value_of<T, kAct>(raw[i], s.up != nullptr));
+  }
+  store_tile<uint32_t, kVec, true, false, kWhole>(v, out, t, id, blockIdx.x, shared);
+}
+
+template <typename T, int kAct, bool kVec, int kRows>
+__global__ __launch_bounds__(16 * kGroup / kRows) void act_tiles_kernel(ActArgs s, int first_id, int rows,
+                                                                        const int32_t* offsets, int experts,
+                                                                        TileOut out) {
   keep_denormals();
-  __shared__ TilePart part;
-  const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup + (threadIdx.x & 15) * kEPL;
-  const TileRows t = tile_rows(offsets, experts, rows, id);
+  __shared__ TileShared<kRows> shared;
+  const int id = first_id + (int)blockIdx.y;
+  const TileRows t = tile_rows(offsets, experts, rows, id, shared);
   if (!t.owned) clear_codes(out, id, blockIdx.x);
   if (t.first >= t.hi) return;   // the same for the whole workgroup
-  Chunk<uint32_t> v[kTileRows];
-#pragma unroll
-  for (int i = 0; i < kTileRows; i++) {
-    const int64_t r = t.first + threadIdx.x / 16 + 16 * i;
-    v[i] = narrow<uint32_t>(r < t.hi ? value_at<T, kVec>(s, r, c) : f32x8{});
-  }
-  store_tile<uint32_t, kVec, true, kStream>(v, out, t, id, blockIdx.x, part);
+  if (kVec && whole_tile(t, blockIdx.x, s.F)) act_tile<T, kAct, kVec, kVec, kRows>(s, t, id, out, shared);
+  else act_tile<T, kAct, kVec, false, kRows>(s, t, id, out, shared);
 }
 
 // ---- backward ----------------------------------------------------------------------------
-// Eight elements of dgate, and of dup, from column c of the halves.
+// Eight elements of dgate and of dup; what is not used is not computed.
 struct Both {
   f32x8 gate, up;
 };
-template <typename T, bool kVec>
-__device__ __forceinline__ Both gradients_at(const ActArgs& s, int64_t r, int c) {
-  const f32x8 g = load_floats<T, kVec>((const T*)s.gate + r * s.ld_gate, c, s.F);
-  const f32x8 da = load_floats<T, kVec>((const T*)s.da + r * s.ld_da, c, s.F);
-  f32x8 a;
-  const f32x8 d = slope_of(s.act, g, &a);
-  if (!s.up) return Both{da * d, f32x8{}};
-  const f32x8 u = load_floats<T, kVec>((const T*)s.up + r * s.ld_up, c, s.F);
-  return Both{da * u * d, da * a};
+template <typename T, int kAct>
+__device__ __forceinline__ Both gradients_of(const Raw<T, true>& v, bool gated) {
+  const f32x8 g = widen<T>(v.gate), da = widen<T>(v.da);
+  f32x8 a, d;
+#pragma unroll
+  for (int i = 0; i < kEPL; i++) {
+    float one;
+    d[i] = slope_of<kAct>(g[i], &one);
+    a[i] = one;
+  }
+  return Both{gated ? da * widen<T>(v.up) * d : da * d, da * a};
 }
 
-// Elements [c, c + 8) of a row [dgate, dup].
-template <typename T, bool kVec>
+// Elements [c, c + 8) of a row [dgate, dup], wherever they lie.
+template <typename T, int kAct, bool kVec>
 __device__ __forceinline__ f32x8 gradient_at(const ActArgs& s, int64_t r, int c) {
-  if (!s.up || c + kEPL <= s.F) return gradients_at<T, kVec>(s, r, c).gate;
-  if (c >= s.F) return gradients_at<T, kVec>(s, r, c - s.F).up;
+  Raw<T, true> v;
+  if (c + kEPL <= s.F || c >= s.F) {
+    load_raw<T, kVec, false>(v, s, r, c < s.F ? c : c - s.F);
+    const Both b = gradients_of<T, kAct>(v, true);
+    return c < s.F ? b.gate : b.up;
+  }
   // across the end of the first half: elements from F on are the first of the second
-  f32x8 v = gradients_at<T, false>(s, r, c).gate;
-  const f32x8 u = gradients_at<T, false>(s, r, 0).up;
+  load_raw<T, false, false>(v, s, r, c);
+  f32x8 out = gradients_of<T, kAct>(v, true).gate;
+  load_raw<T, false, false>(v, s, r, 0);
+  const f32x8 u = gradients_of<T, kAct>(v, true).up;
   const int n = s.F - c;
 #pragma unroll
   for (int i = 0; i < kEPL; i++) {
 #pragma unroll
     for (int j = 0; j < kEPL; j++)
-      if (i == n + j) v[i] = u[j];
+      if (i == n + j) out[i] = u[j];
   }
-  return v;
+  return out;
 }
 
-// kBoth: a workgroup takes the same 128 columns of both halves (F is a multiple of 128), which reads them once;
-// otherwise 128 columns of the result, wherever they lie.
-template <typename T, bool kVec, bool kBoth, bool kStream>
-__global__ __launch_bounds__(kTileThreads) void act_backward_kernel(ActArgs s, int first_id, int rows,
-                                                                    const int32_t* offsets, int experts, TileOut out) {
+// What a workgroup takes: the same 128 columns of both halves, which reads them once; or 128 columns of the result, which
+// lie in one of the halves or across their border.
+enum Part { kBothHalves, kGateHalf, kUpHalf, kBorder };
+
+template <typename T, int kAct, bool kVec, Part kPart, bool kWhole, int kRows>
+__device__ __forceinline__ void act_backward_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
+                                                  TileShared<kRows>& shared) {
+  constexpr int kStep = kGroup / kRows;
+  Chunk<uint32_t> v[kRows], u[kPart == kBothHalves ? kRows : 1];
+  if constexpr (kPart != kBorder) {
+    constexpr int kAtOnce = sizeof(T) == 2 ? kRows : kRows / 2;   // rows whose operands are on their way at once
+    Walk<T, kVec, kVec && sizeof(T) == 2 && kPart == kBothHalves, true, kWhole, kStep> walk(s, t, blockIdx.x * kGroup - (kPart == kUpHalf ? s.F : 0));
+#pragma unroll
+    for (int i0 = 0; i0 < kRows; i0 += kAtOnce) {
+      Raw<T, true> raw[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) walk.next(raw[i]);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; i++) {
+        const Both b = gradients_of<T, kAct>(raw[i], s.up != nullptr);
+        v[i0 + i] = narrow<uint32_t>(kPart == kUpHalf ? b.up : b.gate);
+        if constexpr (kPart == kBothHalves) u[i0 + i] = narrow<uint32_t>(b.up);
+      }
+    }
+  } else {
+    const int c = blockIdx.x * kGroup + (threadIdx.x & 15) * kEPL;
+#pragma unroll 1
+    for (int i = 0; i < kRows; i++) {
+      const int64_t r = t.first + threadIdx.x / 16 + kStep * i;
+      const Chunk<uint32_t> one = narrow<uint32_t>(r < t.hi && c < out.K ? gradient_at<T, kAct, kVec>(s, r, c) : f32x8{});
+#pragma unroll
+      for (int j = 0; j < kRows; j++)
+        if (i == j) v[j] = one;
+    }
+  }
+  store_tile<uint32_t, kVec, true, false, kWhole>(v, out, t, id, blockIdx.x, shared);
+  if constexpr (kPart == kBothHalves)
+    store_tile<uint32_t, kVec, true, false, kWhole, true>(u, out, t, id, blockIdx.x + s.F / kGroup, shared);
+}
+
+template <typename T, int kAct, bool kVec, bool kBoth, int kRows>
+__global__ __launch_bounds__(16 * kGroup / kRows) void act_backward_kernel(ActArgs s, int first_id, int rows,
+                                                                           const int32_t* offsets, int experts,
+                                                                           TileOut out) {
   keep_denormals();
-  __shared__ TilePart part;
-  const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup + (threadIdx.x & 15) * kEPL;
-  const TileRows t = tile_rows(offsets, experts, rows, id);
+  __shared__ TileShared<kRows> shared;
+  const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup;
+  const TileRows t = tile_rows(offsets, experts, rows, id, shared);
   if (!t.owned) {
     clear_codes(out, id, blockIdx.x);
     if (kBoth) clear_codes(out, id, blockIdx.x + s.F / kGroup);
   }
-  if (t.first >= t.hi) return;   // the same for the whole workgroup
-  Chunk<uint32_t> v[kTileRows], u[kBoth ? kTileRows : 1];
-#pragma unroll
-  for (int i = 0; i < kTileRows; i++) {
-    const int64_t r = t.first + threadIdx.x / 16 + 16 * i;
-    if constexpr (kBoth) {
-      const Both b = r < t.hi ? gradients_at<T, kVec>(s, r, c) : Both{};
-      v[i] = narrow<uint32_t>(b.gate);
-      u[i] = narrow<uint32_t>(b.up);
-    } else {
-      v[i] = narrow<uint32_t>(r < t.hi && c < out.K ? gradient_at<T, kVec>(s, r, c) : f32x8{});
-    }
-  }
-  store_tile<uint32_t, kVec, true, kStream>(v, out, t, id, blockIdx.x, part);
+  if (t.first >= t.hi) return;   // all of this is the same for the whole workgroup
+  const bool whole = kVec && whole_tile(t, blockIdx.x, kBoth ? s.F : out.K);
   if constexpr (kBoth) {
-    __syncthreads();
-    store_tile<uint32_t, kVec, true, kStream>(u, out, t, id, blockIdx.x + s.F / kGroup, part);
+    if (whole) act_backward_tile<T, kAct, kVec, kBothHalves, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kBothHalves, false, kRows>(s, t, id, out, shared);
+  } else if (c + kGroup <= s.F || !s.up) {
+    if (whole) act_backward_tile<T, kAct, kVec, kGateHalf, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kGateHalf, false, kRows>(s, t, id, out, shared);
+  } else if (c >= s.F) {
+    if (whole) act_backward_tile<T, kAct, kVec, kUpHalf, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kUpHalf, false, kRows>(s, t, id, out, shared);
+  } else {
+    act_backward_tile<T, kAct, kVec, kBorder, false, kRows>(s, t, id, out, shared);
   }
 }
 
@@ -224,7 +310,7 @@ int check_operands(const ActArgs& a, int64_t rows, int64_t F, mxq_dtype dt, bool
   return MXQ_OK;
 }
 
-template <typename T>
+template <typename T, int kAct>
 int launch_rows(const ActArgs& a, int64_t rows, bool vec, uint8_t* data, int64_t ld_data, uint8_t* scale,
                 int64_t scale_ld, hipStream_t stream) {
   const int64_t groups = groups_of(a.F), step = rows_per_launch(groups * 16);
@@ -236,10 +322,10 @@ int launch_rows(const ActArgs& a, int64_t rows, bool vec, uint8_t* data, int64_t
     s.gate = (const T*)a.gate + r * a.ld_gate;
     if (a.up) s.up = (const T*)a.up + r * a.ld_up;
     if (vec)
-      hipLaunchKernelGGL((act_rows_kernel<T, true>), grid, dim3(kRowThreads), 0, stream, s, d, (uint32_t)total,
+      hipLaunchKernelGGL((act_rows_kernel<T, kAct, true>), grid, dim3(kRowThreads), 0, stream, s, d, (uint32_t)total,
                          data + r * ld_data, ld_data, scale + r * scale_ld, scale_ld);
     else
-      hipLaunchKernelGGL((act_rows_kernel<T, false>), grid, dim3(kRowThreads), 0, stream, s, d, (uint32_t)total,
+      hipLaunchKernelGGL((act_rows_kernel<T, kAct, false>), grid, dim3(kRowThreads), 0, stream, s, d, (uint32_t)total,
                          data + r * ld_data, ld_data, scale + r * scale_ld, scale_ld);
     const int st = launch_status();
     if (st != MXQ_OK) return st;
@@ -247,31 +333,31 @@ int launch_rows(const ActArgs& a, int64_t rows, bool vec, uint8_t* data, int64_t
   return MXQ_OK;
 }
 
-template <typename T>
+// Rows a lane: four, in workgroups of 512, forward; eight, in workgroups of 256, backward, where four take 131 registers
+// and so leave one workgroup a CU.  49152 x 1024 forward 53.9 us (eight: 54.6), backward 92.8 (four: 112.9).
+constexpr int kForwardRows = 4, kBackwardRows = 8;
+
+template <typename T, int kAct>
 int launch_tiles(const ActArgs& a, int64_t rows, bool vec, const int32_t* offsets, int64_t experts, const TileOut& out,
                  hipStream_t stream) {
   const int64_t tiles = out.code_rows + (offsets ? 2 : 0);   // the rows of no expert, behind and before the others, may take two more
   constexpr int64_t kStep = 65535;   // of a grid's second dimension
   const bool both = a.da && a.up && a.F % kGroup == 0;
-  const bool big = rows * out.K > kStreamBytes;
   const int64_t columns = both ? a.F / kGroup : groups_of(out.K);
-  const dim3 block(kTileThreads);
-#define MXQ_ACT_LAUNCH(...)                                                                                       \
-  hipLaunchKernelGGL((__VA_ARGS__), grid, block, 0, stream, a, (int)t, (int)rows, offsets, (int)experts, out)
+#define MXQ_ACT_LAUNCH(kRows, ...)                                                                                     \
+  hipLaunchKernelGGL((__VA_ARGS__, kRows>), grid, dim3(16 * kGroup / kRows), 0, stream, a, (int)t, (int)rows, offsets, \
+                     (int)experts, out)
   for (int64_t t = 0; t < tiles; t += kStep) {
     const dim3 grid((uint32_t)columns, (uint32_t)std::min(kStep, tiles - t));
     if (!a.da) {
-      if (!vec) MXQ_ACT_LAUNCH(act_tiles_kernel<T, false, false>);
-      else if (big) MXQ_ACT_LAUNCH(act_tiles_kernel<T, true, true>);
-      else MXQ_ACT_LAUNCH(act_tiles_kernel<T, true, false>);
+      if (vec) MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, true);
+      else MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, false);
     } else if (both) {
-      if (!vec) MXQ_ACT_LAUNCH(act_backward_kernel<T, false, true, false>);
-      else if (big) MXQ_ACT_LAUNCH(act_backward_kernel<T, true, true, true>);
-      else MXQ_ACT_LAUNCH(act_backward_kernel<T, true, true, false>);
+      if (vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, true);
+      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, true);
     } else {
-      if (!vec) MXQ_ACT_LAUNCH(act_backward_kernel<T, false, false, false>);
-      else if (big) MXQ_ACT_LAUNCH(act_backward_kernel<T, true, false, true>);
-      else MXQ_ACT_LAUNCH(act_backward_kernel<T, true, false, false>);
+      if (vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, false);
+      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, false);
     }
     const int st = launch_status();
     if (st != MXQ_OK) return st;
@@ -279,6 +365,17 @@ int launch_tiles(const ActArgs& a, int64_t rows, bool vec, const int32_t* offset
 #undef MXQ_ACT_LAUNCH
   return MXQ_OK;
 }
+
+// The call for the activation and the type at hand.
+#define MXQ_ACT_DISPATCH(fn, ...)                                                                        \
+  switch (a.act * 2 + (dt == MXQ_FP32)) {                                                                \
+    case MXQ_SILU * 2: return fn<uint16_t, MXQ_SILU>(__VA_ARGS__);                                       \
+    case MXQ_SILU * 2 + 1: return fn<uint32_t, MXQ_SILU>(__VA_ARGS__);                                   \
+    case MXQ_GELU_TANH * 2: return fn<uint16_t, MXQ_GELU_TANH>(__VA_ARGS__);                             \
+    case MXQ_GELU_TANH * 2 + 1: return fn<uint32_t, MXQ_GELU_TANH>(__VA_ARGS__);                         \
+    case MXQ_RELU2 * 2: return fn<uint16_t, MXQ_RELU2>(__VA_ARGS__);                                     \
+    default: return fn<uint32_t, MXQ_RELU2>(__VA_ARGS__);                                                \
+  }
 
 int tile_entry(const ActArgs& a, int64_t rows, int64_t F, mxq_dtype dt, const int32_t* offsets, int64_t experts,
                uint8_t* row_data, int64_t ld_row, uint8_t* row_scale, int64_t row_scale_ld, uint8_t* col_data,
@@ -300,8 +397,7 @@ int tile_entry(const ActArgs& a, int64_t rows, int64_t F, mxq_dtype dt, const in
   const bool vec = F % kEPL == 0 && wide_rows(a.gate, a.ld_gate, dt) && wide_rows(a.up, a.ld_up, dt) && wide_rows(a.da, a.ld_da, dt) &&
                    wide_payload(row_data, ld_row) && wide_payload(col_data, ld_col);
   const TileOut out{(int)K, (int)code_rows, row_data, ld_row, row_scale, row_scale_ld, col_data, ld_col, col_scale, col_scale_ld};
-  return dt == MXQ_BF16 ? launch_tiles<uint16_t>(a, rows, vec, offsets, experts, out, stream)
-                        : launch_tiles<uint32_t>(a, rows, vec, offsets, experts, out, stream);
+  MXQ_ACT_DISPATCH(launch_tiles, a, rows, vec, offsets, experts, out, stream)
 }
 
 }  // namespace
@@ -322,8 +418,7 @@ int mxq_activate_fp8_group128(const void* gate, int64_t ld_gate, const void* up,
   if (!all_ok({rd, rs})) return MXQ_ERR_SHAPE;
   if (!disjoint({rd, rs}, {in.gate, in.up})) return MXQ_ERR_ALIAS;
   const bool vec = F % kEPL == 0 && wide_rows(gate, ld_gate, dt) && wide_rows(up, ld_up, dt) && wide_payload(data, ld_data);
-  return dt == MXQ_BF16 ? launch_rows<uint16_t>(a, rows, vec, data, ld_data, scale, scale_ld, stream)
-                        : launch_rows<uint32_t>(a, rows, vec, data, ld_data, scale, scale_ld, stream);
+  MXQ_ACT_DISPATCH(launch_rows, a, rows, vec, data, ld_data, scale, scale_ld, stream)
 }
 
 int mxq_activate_fp8_group128_row_col(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int64_t rows,

@@ -32,6 +32,12 @@ constexpr uint32_t kPoison4 = 0x7F7F7F7Fu;
 constexpr int kModeFpDenorm = 1 | (4 << 6) | (3 << 11);
 __device__ __forceinline__ void keep_denormals() { __builtin_amdgcn_s_setreg(kModeFpDenorm, 0xF); }
 
+// The larger magnitude of two fp32 values, a NaN if one of them is: one instruction for three values.
+__device__ __forceinline__ float larger(float a, float b) {
+  return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
+}
+__device__ __forceinline__ uint32_t magnitude_bits(float m) { return __builtin_bit_cast(uint32_t, m) & 0x7FFFFFFFu; }
+
 // Eight elements of a row as their bit patterns.
 template <typename T>
 struct Chunk {
@@ -43,15 +49,22 @@ struct Chunk {
     else return w[i] & 0x7FFFFFFFu;
   }
   __device__ __forceinline__ uint32_t amax() const {
+    if constexpr (sizeof(T) == 4) {
+      float m = value(0);
+#pragma unroll
+      for (int i = 1; i < kEPL; i++) m = larger(m, value(i));
+      return magnitude_bits(m);
+    }
     uint32_t m = mag(0);
 #pragma unroll
     for (int i = 1; i < kEPL; i++) m = max(m, mag(i));
     return m;
   }
+  __device__ __forceinline__ float value(int i) const { return __builtin_bit_cast(float, w[i]); }   // of fp32
   // Four payload bytes of elements 4 h .. 4 h + 3 at scale 2^(code - 127).
   __device__ __forceinline__ uint32_t e4m3x4(int h, uint32_t code) const {
     const float s = __builtin_bit_cast(float, code << 23);   // code 0 stands for 2^-127 here
-    s16x2 r{0, 0};
+    s16x2 r = __builtin_nondeterministic_value(r);           // both halves are written
     if constexpr (sizeof(T) == 2) {
       r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[2 * h]), s, false);
       r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[2 * h + 1]), s, true);
@@ -73,15 +86,17 @@ __device__ __forceinline__ uint32_t code_of(uint32_t amax) {
   return amax >= kInf ? 255u : (uint32_t)max(code, 0);
 }
 
-// Elements [c, c + 8) of a row of K; those from K on are 0.
-template <typename T, bool kVec>
+// Elements [c, c + 8) of a row of K; those from K on are 0.  kOnce: with the non-temporal hint, for rows that nothing
+// reads again soon.
+template <typename T, bool kVec, bool kOnce = false>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int K) {
   Chunk<T> v;
   if (kVec) {
     if (c < K) {
       const u32x4* p = reinterpret_cast<const u32x4*>(row + c);
 #pragma unroll
-      for (int i = 0; i < Chunk<T>::kWords / 4; i++) reinterpret_cast<u32x4*>(v.w)[i] = p[i];
+      for (int i = 0; i < Chunk<T>::kWords / 4; i++)
+        reinterpret_cast<u32x4*>(v.w)[i] = kOnce ? __builtin_nontemporal_load(p + i) : p[i];
       return v;
     }
 #pragma unroll
@@ -125,6 +140,14 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, dpp<0x140>(v));   // row_mirror
 }
 
+// Lane rows (16 lanes) 1 and 3 of a change places with rows 0 and 2 of b; the upper half of a with the lower of b.
+__device__ __forceinline__ u32x2 swap16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+}
+__device__ __forceinline__ u32x2 swap32(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+}
+
 template <typename T>
 __device__ __forceinline__ u32x2 payload_of(const Chunk<T>& v, uint32_t code) {
   if (code == 255u) return u32x2{kPoison4, kPoison4};
@@ -133,9 +156,9 @@ __device__ __forceinline__ u32x2 payload_of(const Chunk<T>& v, uint32_t code) {
 
 // ---- groups along the columns, and along both -------------------------------------------
 // A workgroup takes a tile of 128 rows x 128 columns, which holds whole groups
-// both ways: 16 lanes across a row, 16 rows at a time, 8 rows a lane, all of it
+// both ways: 16 lanes across a row, 16 or 32 rows at a time, 8 or 4 rows a lane, all of it
 // in registers.  A column's largest magnitude is reduced over a lane's rows, over
-// the wave's four lane rows and, through LDS, over the four waves.
+// the wave's four lane rows and, through LDS, over the waves.
 constexpr int kTileThreads = 256, kTileRows = kGroup / (kTileThreads / 16);
 // Payloads of more than the L2s hold (32 MiB) leave with the non-temporal hint:
 // 5000 x 8192 bf16 both ways 36.2 -> 30.6 us, 8192 x 8192 fp32 76 -> 72 us, bf16
@@ -153,99 +176,160 @@ struct TileOut {
   uint8_t* col_scale;
   int64_t col_scale_ld;
 };
-typedef uint32_t TilePart[kTileThreads / 64][kGroup];   // in LDS
-
 // Rows of a tile: `first` to `hi`; owned: they are an expert's (or there are no experts).
 struct TileRows {
   int64_t first, hi;
   bool owned;
+  __device__ __forceinline__ int have() const { return (int)min(hi - first, (int64_t)kGroup); }
 };
-__device__ __forceinline__ TileRows tile_rows(const int32_t* offsets, int experts, int rows, int id) {
-  Segment s{0, id, 0, rows, 0};
-  if (offsets) s = find_tile<kGroup>(offsets, experts, rows, id);
-  return TileRows{(int64_t)s.lo + (int64_t)s.tile * kGroup, s.hi, !offsets || s.expert < experts};
+
+// In LDS, for a workgroup whose lanes hold kRows rows each: 256 lanes with eight or 512 with four.
+template <int kRows>
+struct TileShared {
+  static constexpr int kThreads = 16 * kGroup / kRows;
+  uint32_t amax[kThreads / 64][kGroup];
+  float scale[kGroup];
+  int poisoned[2];   // of the first and of the second matrix that the workgroup stores
+  TileRows rows;
+};
+
+// The rows of tile `id`, found by the first wave for all.  Every lane calls it, before store_tile.
+template <int kRows>
+__device__ __forceinline__ TileRows tile_rows(const int32_t* offsets, int experts, int rows, int id,
+                                              TileShared<kRows>& sh) {
+  if (threadIdx.x < 2) sh.poisoned[threadIdx.x] = 0;   // seen by all behind store_tile's first barrier
+  if (!offsets) return TileRows{(int64_t)id * kGroup, rows, true};
+  if (threadIdx.x < 64) {
+    const Segment s = find_tile<kGroup>(offsets, experts, rows, id);
+    if (threadIdx.x == 0) sh.rows = TileRows{(int64_t)s.lo + (int64_t)s.tile * kGroup, s.hi, s.expert < experts};
+  }
+  __syncthreads();
+  // the same for all lanes, and known to be
+  const auto uniform = [](int64_t v) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+           (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
+  };
+  return TileRows{uniform(sh.rows.first), uniform(sh.rows.hi), __builtin_amdgcn_readfirstlane((int)sh.rows.owned) != 0};
 }
 
 // The code row of a tile that no expert owns is one that no group needs: zeros in the columns of tile column `at`.
 __device__ __forceinline__ void clear_codes(const TileOut& o, int id, int at) {
-  const int c = at * kGroup + (threadIdx.x & 15) * kEPL;
-  if (id < o.code_rows && threadIdx.x / 16 == 0) {
+  const int c = at * kGroup + (int)threadIdx.x;
+  if (id < o.code_rows && threadIdx.x < kGroup && c < o.K) o.col_scale[(int64_t)id * o.col_scale_ld + c] = 0;
+}
+
+// Payloads and codes of the tile in tile column `at` of which this lane holds every kStep-th row from row16 on (zeros
+// where there is no such row).  All lanes of the workgroup call it, once, or a second time with kSecond.  kWhole: the tile
+// has 128 rows and 128 columns.
+template <typename T, bool kVec, bool kRow, bool kStream, bool kWhole, bool kSecond = false, int kRows>
+__device__ __forceinline__ void store_tile(const Chunk<T> (&v)[kRows], const TileOut& o, const TileRows& t, int id,
+                                           int at, TileShared<kRows>& sh) {
+  constexpr int kStep = kGroup / kRows;
+  const int lane16 = threadIdx.x & 15, row16 = threadIdx.x / 16, wave = threadIdx.x / 64;
+  const int c = at * kGroup + lane16 * kEPL;
+  const int have = kWhole ? kGroup : t.have();
+  if constexpr (kRow) {
+    uint8_t* p = o.row_data + t.first * o.ld_row + row16 * o.ld_row;
+    uint32_t mine = 0;   // lane i of the 16 stores the code of their i-th row
 #pragma unroll
-    for (int i = 0; i < kEPL; i++)
-      if (c + i < o.K) o.col_scale[(int64_t)id * o.col_scale_ld + c + i] = 0;
+    for (int i = 0; i < kRows; i++) {
+      const uint32_t code = code_of<T>(max16(v[i].amax()));
+      if (kWhole || row16 + kStep * i < have) store_chunk<kVec, kStream>(p, c, kWhole ? c + 1 : o.K, payload_of(v[i], code));
+      mine = lane16 == i ? code : mine;
+      p += kStep * o.ld_row;
+    }
+    const int r = row16 + kStep * lane16;
+    if (lane16 < kRows && (kWhole || r < have)) o.row_scale[t.first * o.row_scale_ld + r * o.row_scale_ld + at] = (uint8_t)mine;
+  }
+  uint8_t* p = o.col_data + t.first * o.ld_col + row16 * o.ld_col;
+  if (!t.owned) {   // the same for the whole workgroup
+#pragma unroll
+    for (int i = 0; i < kRows; i++) {
+      if (kWhole || row16 + kStep * i < have) store_chunk<kVec, kStream>(p, c, kWhole ? c + 1 : o.K, u32x2{0, 0});
+      p += kStep * o.ld_col;
+    }
+    return;
+  }
+  uint32_t m[kEPL];
+#pragma unroll
+  for (int j = 0; j < kEPL; j++) {
+    if constexpr (sizeof(T) == 4) {
+      float f = v[0].value(j);
+#pragma unroll
+      for (int i = 1; i < kRows; i++) f = larger(f, v[i].value(j));
+      m[j] = magnitude_bits(f);
+    } else {
+      m[j] = v[0].mag(j);
+#pragma unroll
+      for (int i = 1; i < kRows; i++) m[j] = max(m[j], v[i].mag(j));
+    }
+  }
+  // The wave's four lane rows: swaps leave lane row q with the whole wave's columns q and 4 + q.
+#pragma unroll
+  for (int j = 0; j < kEPL; j += 2) {
+    const u32x2 s = swap16(m[j], m[j + 1]);
+    m[j / 2] = max(s[0], s[1]);
+  }
+#pragma unroll
+  for (int j = 0; j < kEPL / 2; j += 2) {
+    const u32x2 s = swap32(m[j], m[j + 1]);
+    sh.amax[wave][lane16 * kEPL + (threadIdx.x & 63) / 16 + 2 * j] = max(s[0], s[1]);
+  }
+  __syncthreads();
+  if (threadIdx.x < kGroup) {   // a column a lane
+    const int k = threadIdx.x;
+    uint32_t amax = sh.amax[0][k];
+#pragma unroll
+    for (int w = 1; w < TileShared<kRows>::kThreads / 64; w++) amax = max(amax, sh.amax[w][k]);
+    const uint32_t code = code_of<T>(amax);
+    sh.scale[k] = __builtin_bit_cast(float, code << 23);   // code 0 stands for 2^-127 here
+    if (code == 255u) sh.poisoned[kSecond] = 1;
+    if (id < o.code_rows && (kWhole || at * kGroup + k < o.K))
+      o.col_scale[(int64_t)id * o.col_scale_ld + at * kGroup + k] = (uint8_t)code;
+  }
+  __syncthreads();
+  float scale[kEPL];
+#pragma unroll
+  for (int j = 0; j < kEPL; j++) scale[j] = sh.scale[lane16 * kEPL + j];
+  u32x2 poison{0, 0};
+  if (sh.poisoned[kSecond]) {   // the same for the whole workgroup
+#pragma unroll
+    for (int j = 0; j < kEPL; j++)
+      if (__builtin_bit_cast(uint32_t, scale[j]) == 255u << 23) poison[j / 4] |= 0xFFu << (8 * (j & 3));
+  }
+  // Two rows at a time: a conversion takes two values of one scale, so a column's pair of rows.
+#pragma unroll
+  for (int i = 0; i < kRows; i += 2) {
+    uint32_t pair[kEPL / 2];   // bytes: row i, row i + 1 of column 2 j, then of column 2 j + 1
+#pragma unroll
+    for (int j = 0; j < kEPL / 2; j++) {
+      s16x2 b = __builtin_nondeterministic_value(b);   // both halves are written
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t lo = __builtin_amdgcn_perm(v[i + 1].w[j], v[i].w[j], 0x05040100u);
+        const uint32_t hi = __builtin_amdgcn_perm(v[i + 1].w[j], v[i].w[j], 0x07060302u);
+        b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, __builtin_bit_cast(bf16x2, lo), scale[2 * j], false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, __builtin_bit_cast(bf16x2, hi), scale[2 * j + 1], true);
+      } else {
+        b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[i].value(2 * j), v[i + 1].value(2 * j), scale[2 * j], false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[i].value(2 * j + 1), v[i + 1].value(2 * j + 1),
+                                                     scale[2 * j + 1], true);
+      }
+      pair[j] = __builtin_bit_cast(uint32_t, b);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const uint32_t pick = k ? 0x07050301u : 0x06040200u;
+      u32x2 q{__builtin_amdgcn_perm(pair[1], pair[0], pick), __builtin_amdgcn_perm(pair[3], pair[2], pick)};
+      q = (q & ~poison) | (poison & kPoison4);
+      if (kWhole || row16 + kStep * (i + k) < have) store_chunk<kVec, kStream>(p, c, kWhole ? c + 1 : o.K, q);
+      p += kStep * o.ld_col;
+    }
   }
 }
 
-// Payloads and codes of the tile in tile column `at` whose rows row16, row16 + 16, ... this lane holds (zeros
-// where there is no such row).  All lanes of the workgroup call it; `part` is free again behind a barrier.
-template <typename T, bool kVec, bool kRow, bool kStream>
-__device__ __forceinline__ void store_tile(const Chunk<T> (&v)[kTileRows], const TileOut& o, const TileRows& t, int id,
-                                           int at, TilePart& part) {
-  const int lane16 = threadIdx.x & 15, row16 = threadIdx.x / 16, wave = threadIdx.x / 64;
-  const int c = at * kGroup + lane16 * kEPL;
-  if constexpr (kRow) {
-#pragma unroll
-    for (int i = 0; i < kTileRows; i++) {
-      const int64_t r = t.first + row16 + 16 * i;
-      const uint32_t code = code_of<T>(max16(v[i].amax()));
-      if (r < t.hi) {
-        store_chunk<kVec, kStream>(o.row_data + r * o.ld_row, c, o.K, payload_of(v[i], code));
-        if (lane16 == 0) o.row_scale[r * o.row_scale_ld + at] = (uint8_t)code;
-      }
-    }
-  }
-  uint32_t code[kEPL];
-  if (t.owned) {   // the same for the whole workgroup
-    uint32_t m[kEPL];
-#pragma unroll
-    for (int j = 0; j < kEPL; j++) {
-      m[j] = v[0].mag(j);
-#pragma unroll
-      for (int i = 1; i < kTileRows; i++) m[j] = max(m[j], v[i].mag(j));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32));
-    }
-    if ((threadIdx.x & 63) < 16) {
-#pragma unroll
-      for (int j = 0; j < kEPL; j++) part[wave][lane16 * kEPL + j] = m[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kEPL; j++) {
-      const int k = lane16 * kEPL + j;
-      code[j] = code_of<T>(max(max(part[0][k], part[1][k]), max(part[2][k], part[3][k])));
-    }
-    if (row16 == 0 && id < o.code_rows) {
-#pragma unroll
-      for (int j = 0; j < kEPL; j++)
-        if (c + j < o.K) o.col_scale[(int64_t)id * o.col_scale_ld + c + j] = (uint8_t)code[j];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kTileRows; i++) {
-    const int64_t r = t.first + row16 + 16 * i;
-    if (r >= t.hi) continue;
-    u32x2 q{0, 0};
-    if (t.owned) {
-#pragma unroll
-      for (int j = 0; j < kEPL; j++) {
-        uint32_t byte = 0x7F;
-        if (code[j] != 255u) {
-          const float sc = __builtin_bit_cast(float, code[j] << 23);
-          s16x2 p{0, 0};
-          if constexpr (sizeof(T) == 2) {
-            const uint32_t one = (v[i].w[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
-            p = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(p, __builtin_bit_cast(bf16x2, one), sc, false);
-          } else {
-            p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, __builtin_bit_cast(float, v[i].w[j]), 0.0f, sc, false);
-          }
-          byte = __builtin_bit_cast(uint32_t, p) & 0xFFu;
-        }
-        q[j / 4] |= byte << (8 * (j & 3));
-      }
-    }
-    store_chunk<kVec, kStream>(o.col_data + r * o.ld_col, c, o.K, q);
-  }
+// Whether the tile in tile column `at` has 128 rows and 128 columns.
+__device__ __forceinline__ bool whole_tile(const TileRows& t, int at, int K) {
+  return t.hi - t.first >= kGroup && (at + 1) * kGroup <= K;
 }
 
 }  // namespace mxq_dev

@@ -62,9 +62,9 @@ template <typename T, bool kVec, bool kRow, bool kStream>
 __global__ __launch_bounds__(kTileThreads) void tile_groups_kernel(Source src, int first_id, int rows,
                                                                    const int32_t* offsets, int experts, TileOut out) {
   keep_denormals();
-  __shared__ TilePart part;
+  __shared__ TileShared<kTileRows> shared;
   const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup + (threadIdx.x & 15) * kEPL;
-  const TileRows t = tile_rows(offsets, experts, rows, id);
+  const TileRows t = tile_rows(offsets, experts, rows, id, shared);
   if (!t.owned) clear_codes(out, id, blockIdx.x);
   if (t.first >= t.hi) return;   // the same for the whole workgroup
   Chunk<T> v[kTileRows];
@@ -74,7 +74,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_groups_kernel(Source src, i
     const int from = r < t.hi ? source_row(src, (int)r) : -1;
     v[i] = load_chunk<T, kVec>((const T*)src.x + (from < 0 ? 0 : from) * src.ld, from < 0 ? out.K : c, out.K);
   }
-  store_tile<T, kVec, kRow, kStream>(v, out, t, id, blockIdx.x, part);
+  if (kVec && whole_tile(t, blockIdx.x, out.K)) store_tile<T, kVec, kRow, kStream, kVec>(v, out, t, id, blockIdx.x, shared);
+  else store_tile<T, kVec, kRow, kStream, false>(v, out, t, id, blockIdx.x, shared);
 }
 
 struct Checked {

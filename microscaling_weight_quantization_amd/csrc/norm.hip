@@ -159,9 +159,9 @@ __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs a) {
 template <typename TX, typename TS, bool kVec, bool kStream>
 __global__ __launch_bounds__(kTileThreads) void norm_columns_kernel(NormArgs a, int first_id, TileOut out) {
   keep_denormals();
-  __shared__ TilePart part;
+  __shared__ TileShared<kTileRows> shared;
   const int id = first_id + (int)blockIdx.y, c = blockIdx.x * kGroup + (threadIdx.x & 15) * kEPL;
-  const TileRows t{(int64_t)id * kGroup, a.rows, true};
+  const TileRows t = tile_rows(nullptr, 0, a.rows, id, shared);
   const f32x8 w = weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
   Chunk<uint32_t> v[kTileRows];
 #pragma unroll
@@ -175,7 +175,8 @@ __global__ __launch_bounds__(kTileThreads) void norm_columns_kernel(NormArgs a, 
     }
     v[i] = narrow<uint32_t>(s * st.r * st.f * w);
   }
-  store_tile<uint32_t, kVec, false, kStream>(v, out, t, id, blockIdx.x, part);
+  if (kVec && whole_tile(t, blockIdx.x, a.K)) store_tile<uint32_t, kVec, false, kStream, kVec>(v, out, t, id, blockIdx.x, shared);
+  else store_tile<uint32_t, kVec, false, kStream, false>(v, out, t, id, blockIdx.x, shared);
 }
 
 // ---- backward ----------------------------------------------------------------------------
