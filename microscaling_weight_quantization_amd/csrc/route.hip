@@ -33,29 +33,71 @@ struct RouteArgs {
   float scale;
   int groups, top_groups, group_top, top_k;
   MxqDivisor group_size;
+  int group_lanes_log, per;   // lanes of a group (2 to this power) and experts of a lane, where 16 lanes share a token
+  bool wide, wide_bias;       // whose experts fill the lanes and can be read 16 bytes at a time
   int32_t* ids;
   float* weights;
 };
 
+constexpr int kThreads = 256;
 constexpr int kMost = 512;            // experts
-constexpr int kPer = kMost / 64;      // a lane
-constexpr int kTokens = 4;            // of a workgroup, a wave each
+constexpr int kPer = kMost / 64;      // of a lane where a wave has a token to itself
 constexpr double kClosed = -__builtin_inf();
-constexpr double kNaN = -1e300;       // a NaN's place among the keys: open, below all others
+constexpr double kNaN = -0x1p990;     // a NaN's place among the keys: open, below all others
+constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.44269504088896341f;
 
-__device__ __forceinline__ float logit_at(const void* row, int e, bool bf16) {
-  return bf16 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t*)row)[e] << 16) : ((const float*)row)[e];
+template <bool kBf16>
+__device__ __forceinline__ float logit_at(const void* row, int e) {
+  return kBf16 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t*)row)[e] << 16) : ((const float*)row)[e];
+}
+template <bool kBf16>
+__device__ __forceinline__ const char* logit_row(const void* logits, int64_t ld, int64_t token) {
+  return (const char*)logits + token * ld * (kBf16 ? 2 : 4);
 }
 
+// ---- a wave to a token, in 64 bits -------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ double row_dpp(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{dpp<CTRL>(b[0]), dpp<CTRL>(b[1])});
+}
+// Lane exchanges between pairs, quads and halves of a row of 16: the last two of values that are equal in the lanes below.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor4 = 0x141, kXor8 = 0x140;
+
+// What two neighbouring rows hold, and the two halves of the wave, in both of them.
+struct Two {
+  double a, b;
+};
+__device__ __forceinline__ Two rows_of_two(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v), lo = swap16(b[0], b[0]), hi = swap16(b[1], b[1]);
+  return Two{__builtin_bit_cast(double, u32x2{lo[0], hi[0]}), __builtin_bit_cast(double, u32x2{lo[1], hi[1]})};
+}
+__device__ __forceinline__ Two halves_of(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v), lo = swap32(b[0], b[0]), hi = swap32(b[1], b[1]);
+  return Two{__builtin_bit_cast(double, u32x2{lo[0], hi[0]}), __builtin_bit_cast(double, u32x2{lo[1], hi[1]})};
+}
+template <typename F>
+__device__ __forceinline__ double wave_fold(double v, F f) {
+  v = f(v, row_dpp<kXor1>(v));
+  v = f(v, row_dpp<kXor2>(v));
+  v = f(v, row_dpp<kXor4>(v));
+  v = f(v, row_dpp<kXor8>(v));
+  Two t = rows_of_two(v);
+  t = halves_of(f(t.a, t.b));
+  return f(t.a, t.b);
+}
 __device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmax(v, __shfl_xor(v, m));
-  return v;
+  return wave_fold(v, [](double a, double b) { return fmax(a, b); });
 }
 __device__ __forceinline__ double wave_add(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+  return wave_fold(v, [](double a, double b) { return a + b; });
+}
+// LDS that the lanes of one wave hand each other.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // The largest of the wave's keys, the lowest index where several are equal; element lane + 64 i is key[i].
@@ -63,18 +105,29 @@ struct Best {
   double key;
   int at;
 };
-__device__ __forceinline__ Best best_of(const double (&key)[kPer]) {
+__device__ __forceinline__ Best better(Best a, Best b) {
+  return b.key > a.key || (b.key == a.key && b.at < a.at) ? b : a;
+}
+template <int CTRL>
+__device__ __forceinline__ Best better_row(Best b) {
+  return better(b, Best{row_dpp<CTRL>(b.key), (int)dpp<CTRL>((uint32_t)b.at)});
+}
+__device__ __forceinline__ Best best_of(const double (&key)[kPer], int count) {
   const int lane = threadIdx.x & 63;
   Best b{key[0], lane};
 #pragma unroll
   for (int i = 1; i < kPer; i++)
-    if (key[i] > b.key) b = Best{key[i], lane + 64 * i};
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const Best o{__shfl_xor(b.key, m), __shfl_xor(b.at, m)};
-    if (o.key > b.key || (o.key == b.key && o.at < b.at)) b = o;
-  }
-  return b;
+    if (64 * i < count && key[i] > b.key) b = Best{key[i], lane + 64 * i};
+  b = better_row<kXor1>(b);
+  b = better_row<kXor2>(b);
+  b = better_row<kXor4>(b);
+  b = better_row<kXor8>(b);
+  Two k = rows_of_two(b.key);
+  u32x2 at = swap16((uint32_t)b.at, (uint32_t)b.at);
+  b = better(Best{k.a, (int)at[0]}, Best{k.b, (int)at[1]});
+  k = halves_of(b.key);
+  at = swap32((uint32_t)b.at, (uint32_t)b.at);
+  return better(Best{k.a, (int)at[0]}, Best{k.b, (int)at[1]});
 }
 __device__ __forceinline__ void take(double (&key)[kPer], int at) {
 #pragma unroll
@@ -82,48 +135,58 @@ __device__ __forceinline__ void take(double (&key)[kPer], int at) {
     if (at == (int)(threadIdx.x & 63) + 64 * i) key[i] = kClosed;
 }
 
-struct RouteShared {
-  double key[kMost], value[kMost];
-  int32_t chosen[kMost];
-  uint8_t kept[kMost];
+// What a wave needs in LDS: keys and values of the experts, the chosen ones, the groups that are kept.
+struct WaveLds {
+  double *key, *value;
+  int32_t* chosen;
+  uint8_t* kept;
+  __host__ __device__ static size_t bytes(int experts, int top_k, int groups) {
+    return ((size_t)experts * 16 + (size_t)top_k * 4 + groups + 15) / 16 * 16;
+  }
+  __device__ __forceinline__ WaveLds(char* lds, const RouteArgs& a) {
+    key = (double*)(lds + threadIdx.x / 64 * bytes(a.experts, a.top_k, a.groups));
+    value = key + a.experts;
+    chosen = (int32_t*)(value + a.experts);
+    kept = (uint8_t*)(chosen + a.top_k);
+  }
 };
 
 template <bool kBf16>
-__global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
-  __shared__ RouteShared shared[kTokens];
-  RouteShared& sh = shared[threadIdx.x / 64];
+__device__ void route_exact(const RouteArgs& a, int64_t token, char* lds) {
+  const WaveLds sh(lds, a);
   const int lane = threadIdx.x & 63;
-  const int64_t token = (int64_t)blockIdx.x * kTokens + threadIdx.x / 64;
-  const bool live = token < a.tokens;
-  const bool open = live && (!a.mask || a.mask[token]);
-  const char* const row = (const char*)a.logits + (live ? token : 0) * a.ld * (kBf16 ? 2 : 4);
-  double l[kPer], key[kPer];
-  double top = kClosed;
+  const bool open = !a.mask || a.mask[token];
+  const char* const row = logit_row<kBf16>(a.logits, a.ld, token);
+  double l[kPer], p[kPer], key[kPer];
+  double top = kClosed, sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int e = lane + 64 * i;
-    l[i] = open && e < a.experts ? (double)logit_at(row, e, kBf16) : kClosed;
+    l[i] = open && e < a.experts ? (double)logit_at<kBf16>(row, e) : kClosed;
     top = fmax(top, l[i]);
   }
   top = wave_max(top);
   if (top == kClosed) top = 0;
-  double sum = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; i++) sum += exp(l[i] - top);
+  for (int i = 0; i < kPer; i++) {
+    if (64 * i >= a.experts) continue;
+    p[i] = exp(a.sigmoid ? -l[i] : l[i] - top);
+    if (a.sigmoid) p[i] = 1 / (1 + p[i]);
+    else sum += p[i];
+  }
   sum = a.sigmoid ? 1.0 : wave_add(sum);
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int e = lane + 64 * i;
-    const double p = a.sigmoid ? 1 / (1 + exp(-l[i])) : exp(l[i] - top) / sum;
     key[i] = l[i];
-    if (a.bias && l[i] != kClosed) key[i] = p + (double)a.bias[e];
+    if (e >= a.experts) continue;
+    if (!a.sigmoid) p[i] /= sum;
+    if (a.bias && l[i] != kClosed) key[i] = p[i] + (double)a.bias[e];
     if (key[i] != key[i]) key[i] = kNaN;
-    if (e < a.experts) {
-      sh.key[e] = key[i];
-      sh.value[e] = a.bias ? key[i] : p;
-    }
+    sh.key[e] = key[i];
+    sh.value[e] = a.bias ? key[i] : p[i];
   }
-  __syncthreads();
+  wave_sync();
   if (a.groups > 1) {
     const int size = a.group_size.d;
     double rank[kPer];
@@ -133,6 +196,7 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
       rank[i] = kClosed;
       if (g < a.groups) {
         double first = kClosed, second = kClosed, v1 = 0, v2 = 0;
+#pragma unroll 4
         for (int j = 0; j < size; j++) {
           const double k = sh.key[g * size + j], v = sh.value[g * size + j];
           if (k > first) second = first, v2 = v1, first = k, v1 = v;
@@ -143,13 +207,14 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
         sh.kept[g] = 0;
       }
     }
+    wave_sync();
     for (int j = 0; j < a.top_groups; j++) {
-      const Best b = best_of(rank);
+      const Best b = best_of(rank, a.groups);
       if (b.key == kClosed) break;
       take(rank, b.at);
       if (lane == 0) sh.kept[b.at] = 1;
     }
-    __syncthreads();
+    wave_sync();
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const int e = lane + 64 * i;
@@ -157,21 +222,21 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
     }
   }
   for (int j = 0; j < a.top_k; j++) {
-    const Best b = best_of(key);
+    const Best b = best_of(key, a.experts);
     take(key, b.at);
     if (lane == 0) sh.chosen[j] = b.key == kClosed ? -1 : b.at;
   }
-  __syncthreads();
+  wave_sync();
   // weights: relative to the largest of the chosen logits where they are made to sum to scale
   double largest = kClosed;
   for (int j = lane; j < a.top_k; j += 64) {
     const int e = sh.chosen[j];
-    if (e >= 0) largest = fmax(largest, (double)logit_at(row, e, kBf16));
+    if (e >= 0) largest = fmax(largest, (double)logit_at<kBf16>(row, e));
   }
   largest = wave_max(largest);
   const auto weight = [&](int e) -> double {
     if (e < 0) return 0.0;
-    const double v = logit_at(row, e, kBf16);
+    const double v = logit_at<kBf16>(row, e);
     if (!a.sigmoid) return a.renormalize ? exp(v - largest) : exp(v - top) / sum;
     const double m = a.renormalize ? fmin(largest, 0.0) : 0.0;
     return v > 0 ? exp(-m) / (1 + exp(-v)) : exp(v - m) / (1 + exp(v));
@@ -180,13 +245,359 @@ __global__ __launch_bounds__(64 * kTokens) void route_kernel(RouteArgs a) {
   for (int j = lane; j < a.top_k; j += 64) total += weight(sh.chosen[j]);
   total = wave_add(total);
   const double scale = a.scale / (a.renormalize && total != 0 ? total : 1.0);
-  if (live)
-    for (int j = lane; j < a.top_k; j += 64) {
-      a.ids[token * a.top_k + j] = sh.chosen[j];
-      a.weights[token * a.top_k + j] = (float)(weight(sh.chosen[j]) * scale);
-    }
+  for (int j = lane; j < a.top_k; j += 64) {
+    a.ids[token * a.top_k + j] = sh.chosen[j];
+    a.weights[token * a.top_k + j] = (float)(weight(sh.chosen[j]) * scale);
+  }
+  wave_sync();   // the LDS may take another token
 }
 
+template <bool kBf16>
+__global__ __launch_bounds__(kThreads) void route_wave_kernel(RouteArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+  if (token < a.tokens) route_exact<kBf16>(a, token, lds);
+}
+
+// ---- sixteen lanes to a token ------------------------------------------------------------
+// Keys are taken in fp32 first, which without a bias is what they are.  A biased score, or the sum of two scores that ranks
+// a group, is known to within a bound; where two that are told apart lie nearer than that, the wave takes its four tokens
+// again in 64 bits, and a token that even so has two within the bound (or a key that is not finite) as above.
+//
+// A key and its expert are one double: the key with the expert's index in the lowest nine bits, so that equal keys fall
+// by index and a comparison moves both.  Each lane sorts its own, and four exchanges between lanes leave the token's
+// largest kList in each of them.
+
+template <int CTRL>
+__device__ __forceinline__ float row_dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+template <typename F>
+__device__ __forceinline__ float row_fold(float v, F f) {
+  v = f(v, row_dpp<kXor1>(v));
+  v = f(v, row_dpp<kXor2>(v));
+  v = f(v, row_dpp<kXor4>(v));
+  return f(v, row_dpp<kXor8>(v));
+}
+template <typename F>
+__device__ __forceinline__ double row_fold(double v, F f) {
+  v = f(v, row_dpp<kXor1>(v));
+  v = f(v, row_dpp<kXor2>(v));
+  v = f(v, row_dpp<kXor4>(v));
+  return f(v, row_dpp<kXor8>(v));
+}
+// A NaN stays.
+__device__ __forceinline__ float high(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float low(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+// These do not meet one.
+__device__ __forceinline__ double high(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double low(double a, double b) { return fmin(a, b); }
+template <typename F>
+__device__ __forceinline__ F row_max(F v) {
+  return row_fold(v, [](F a, F b) { return high(a, b); });
+}
+template <typename F>
+__device__ __forceinline__ F row_min(F v) {
+  return row_fold(v, [](F a, F b) { return low(a, b); });
+}
+template <typename F>
+__device__ __forceinline__ F row_add(F v) {
+  return row_fold(v, [](F a, F b) { return a + b; });
+}
+__device__ __forceinline__ bool row_any(bool v) { return row_max(v ? 1.0f : 0.0f) != 0; }
+
+// Of two numbers (none of these is a NaN, so nothing needs to be made quiet first).
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ void order(double& a, double& b) {
+  const double x = max64(a, b);
+  asm("v_min_f64 %0, %1, %2" : "=v"(b) : "v"(a), "v"(b));
+  a = x;
+}
+
+// Falling order of n values that first rise and then fall, or the other way round.
+template <int n>
+__device__ __forceinline__ void merge_bitonic(double* v) {
+#pragma unroll
+  for (int d = n / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < n; i++)
+      if (!(i & d)) order(v[i], v[i + d]);
+}
+// Falling order of n values: Batcher's merging of odd and even places.
+template <int n>
+__device__ __forceinline__ void sort_falling(double* v) {
+#pragma unroll
+  for (int p = 1; p < n; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < n; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; i++)
+          if (j + i + k < n && (j + i) / (2 * p) == (j + i + k) / (2 * p)) order(v[j + i], v[j + i + k]);
+}
+
+constexpr double kOpen = -0x1p995, kShut = -0x1p1000, kHuge = 0x1p990;   // open keys lie above kOpen
+
+__device__ __forceinline__ double with_index(double key, int e) {
+  // infinities become numbers
+  const double v = fmin(fmax(key, kShut), kHuge);
+  u32x2 b = __builtin_bit_cast(u32x2, v);
+  b[0] = (b[0] & ~(uint32_t)(kMost - 1)) | (uint32_t)(e ^ (v < 0 ? 0 : kMost - 1));
+  return __builtin_bit_cast(double, b);
+}
+__device__ __forceinline__ int index_of(double v) {
+  return (int)(__builtin_bit_cast(u32x2, v)[0] & (kMost - 1)) ^ (v < 0 ? 0 : kMost - 1);
+}
+
+// Steps that the list of a token takes through the row's other lanes.
+template <int CTRL, int kList>
+__device__ __forceinline__ void merge_lanes(double (&v)[kList]) {
+  double o[kList];
+#pragma unroll
+  for (int i = 0; i < kList; i++) o[i] = row_dpp<CTRL>(v[i]);
+#pragma unroll
+  for (int i = 0; i < kList; i++) v[i] = max64(v[i], o[kList - 1 - i]);
+  merge_bitonic<kList>(v);
+}
+
+// The largest kList of n values, falling.
+template <int n, int kList>
+__device__ __forceinline__ void largest_of(const double (&d)[n], double (&v)[kList]) {
+  constexpr int kFirst = n < kList ? n : kList;
+#pragma unroll
+  for (int i = 0; i < kList; i++) v[i] = i < kFirst ? d[i < n ? i : 0] : kShut;
+  sort_falling<kFirst>(v);
+#pragma unroll
+  for (int at = kList; at < n; at += kList) {
+    double o[kList];
+#pragma unroll
+    for (int i = 0; i < kList; i++) o[i] = d[at + i < n ? at + i : 0];
+    sort_falling<kList>(o);
+#pragma unroll
+    for (int i = 0; i < kList; i++) v[i] = max64(v[i], o[kList - 1 - i]);
+    merge_bitonic<kList>(v);
+  }
+}
+
+// How many groups go before this lane's: those of a larger value, or of an equal one and a lower index.
+template <int N, typename F>
+__device__ __forceinline__ int groups_before(F v, int g, int group_lanes) {
+  int before = 0;
+  if constexpr (N < 16) {
+    before = groups_before<N + 1>(v, g, group_lanes);
+    if ((N & (group_lanes - 1)) == 0) {
+      const F o = row_dpp<0x120 + N>(v);   // rotated by N lanes
+      const int og = (int)dpp<0x120 + N>((uint32_t)g);
+      before += o > v || (o == v && og < g);
+    }
+  }
+  return before;
+}
+
+// How scores are computed in fp32 and in 64 bits, and how far two of them may be off together: a sigmoid by 4 steps of 1 each, a
+// softmax by its up to 36 roundings of the sum, in parts of the largest score; a key by its own rounding and, in 64 bits, by
+// the nine bits of the index.
+template <typename F>
+struct Score;
+template <>
+struct Score<float> {
+  static constexpr float kSigmoid = 0x1p-20f, kSoftmax = 0x1p-17f, kKey = 0x1p-22f, kInfinite = __builtin_inff();
+  static __device__ __forceinline__ float exponential(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
+  static __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
+};
+template <>
+struct Score<double> {
+  static constexpr double kSigmoid = 0x1p-49, kSoftmax = 0x1p-46, kKey = 0x1p-41, kInfinite = __builtin_inf();
+  static __device__ __forceinline__ double exponential(double v) { return exp(v); }
+  static __device__ __forceinline__ double inverse(double v) { return 1 / v; }
+};
+
+// A lane's experts: base, base + 1, ...; x their logits, -inf where there is none or it is closed; bias theirs.
+template <int kEach>
+struct Mine {
+  int lane16, group, base;
+  float x[kEach], bias[kEach];
+};
+
+// Lane j's pick, the token's j-th expert with its key, into *pick.  Returns whether the choice is in doubt.
+template <typename F, int kList, int kEach>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m, float top, double* pick) {
+  using S = Score<F>;
+  const bool sums = a.groups > 1 && a.group_top == 2;      // groups rank by scores
+  bool doubt = false;
+  F s[kEach], bound = S::kSigmoid;
+  if (a.bias || sums) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < kEach; i++) s[i] = S::inverse(1 + S::exponential(-(F)m.x[i]));
+    } else {
+      F sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; i++) {
+        s[i] = S::exponential((F)m.x[i] - (F)top);
+        sum += s[i];
+      }
+      sum = row_add(sum);
+      const F r = sum > 0 ? 1 / sum : (F)0;
+      bound = S::kSoftmax * r;
+#pragma unroll
+      for (int i = 0; i < kEach; i++) s[i] *= r;
+    }
+  }
+  F key[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; i++) {
+    key[i] = m.x[i];
+    if (a.bias) {
+      key[i] = m.x[i] == -kInf ? -S::kInfinite : s[i] + (F)m.bias[i];
+      doubt |= !(key[i] < S::kInfinite);
+    }
+  }
+  bool kept = true;
+  if (a.groups > 1) {
+    const int lanes = 1 << a.group_lanes_log;
+    F first = -S::kInfinite, second = first;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      const F v = sums && !a.bias ? (m.x[i] == -kInf ? -S::kInfinite : s[i]) : key[i];
+      second = fmax(second, fmin(first, v));
+      first = fmax(first, v);
+    }
+    const auto fold = [&](F f, F o) {
+      second = fmax(fmax(second, o), fmin(first, f));
+      first = fmax(first, f);
+    };
+    if (lanes > 1) fold(row_dpp<kXor1>(first), row_dpp<kXor1>(second));
+    if (lanes > 2) fold(row_dpp<kXor2>(first), row_dpp<kXor2>(second));
+    if (lanes > 4) fold(row_dpp<kXor4>(first), row_dpp<kXor4>(second));
+    const F rank = sums && second != -S::kInfinite ? first + second : first;
+    kept = groups_before<1>(rank, m.group, lanes) < a.top_groups;
+    if (a.bias || sums) {
+      const F least = row_min(kept ? rank : S::kInfinite), most = row_max(kept ? -S::kInfinite : rank);
+      doubt |= most > -S::kInfinite && !(least - most >= 2 * bound + (fabs(least) + fabs(most)) * S::kKey);
+    }
+  }
+  double d[kEach], v[kList];
+#pragma unroll
+  for (int i = 0; i < kEach; i++)   // + 0: of the zeros one is as good as the other
+    d[i] = with_index(kept ? (double)(key[i] + 0) : -S::kInfinite, min(m.base + i, kMost - 1));
+  largest_of<kEach, kList>(d, v);
+  merge_lanes<kXor1>(v);
+  merge_lanes<kXor2>(v);
+  merge_lanes<kXor4>(v);
+  merge_lanes<kXor8>(v);
+  double mine = v[0];
+#pragma unroll
+  for (int j = 1; j < kList; j++) mine = m.lane16 == j ? v[j] : mine;
+  *pick = mine;
+  if (a.bias) {
+    const bool has = m.lane16 < a.top_k && mine > kOpen;
+    const F k = (F)mine, next = (F)row_dpp<0x101>(mine);   // of the next lane
+    const F step = bound + fabs(k) * S::kKey;
+    doubt |= has && m.lane16 + 1 < a.top_k && next > (F)kOpen && k - next < step;
+    // and the last of them against those that are left out: how many keys lie above it less the step
+    const F edge = row_min(has ? k - step : S::kInfinite);
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) above += kept && key[i] >= edge;
+    doubt |= row_add((float)above) > (float)a.top_k;
+  }
+  return row_any(doubt);
+}
+
+// A lane's row of experts, kAt of them in 16 bytes; those from `count` on -inf.
+template <int kEach, bool kBf16>
+__device__ __forceinline__ void load_wide(float (&x)[kEach], const char* p, int count) {
+  constexpr int kAt = kBf16 ? 8 : 4;
+#pragma unroll
+  for (int i = 0; i < kEach; i += kAt) {
+    const u32x4 w = i < count ? *(const u32x4*)(p + i * (kBf16 ? 2 : 4)) : u32x4{};
+#pragma unroll
+    for (int j = 0; j < kAt && i + j < kEach; j++) {
+      const uint32_t bits = kBf16 ? (j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16) : w[j % 4];
+      x[i + j] = i < count ? __builtin_bit_cast(float, bits) : -kInf;
+    }
+  }
+}
+
+template <int kEach, int kList, bool kBf16>
+__global__ __launch_bounds__(kThreads) void route_row_kernel(RouteArgs a) {
+  keep_denormals();
+  extern __shared__ __align__(16) char lds[];
+  Mine<kEach> m;
+  m.lane16 = threadIdx.x & 15;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  const bool live = token < a.tokens, open = live && (!a.mask || a.mask[token]);
+  const char* const row = logit_row<kBf16>(a.logits, a.ld, live ? token : 0);
+  m.group = m.lane16 >> a.group_lanes_log;
+  const int in_group = (m.lane16 & ((1 << a.group_lanes_log) - 1)) * a.per;
+  m.base = m.group * (int)a.group_size.d + in_group;
+  const int here = min(a.per, (int)a.group_size.d - in_group), count = open ? here : 0;
+  if (a.wide) {
+    load_wide<kEach, kBf16>(m.x, row + m.base * (kBf16 ? 2 : 4), count);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; i++) m.x[i] = i < count ? logit_at<kBf16>(row, m.base + i) : -kInf;
+  }
+  if (a.bias && a.wide_bias) {
+    load_wide<kEach, false>(m.bias, (const char*)(a.bias + m.base), here);
+  } else if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < kEach; i++) m.bias[i] = i < here ? a.bias[m.base + i] : 0.0f;
+  }
+  float top = m.x[0];
+#pragma unroll
+  for (int i = 1; i < kEach; i++) top = high(top, m.x[i]);
+  top = row_max(top);
+  const bool odd = !(top < kInf);   // a NaN or +Inf among the logits
+  if (top == -kInf) top = 0;
+  double mine;
+  bool again = choose<float, kList>(a, m, top, &mine) && !odd;
+  if (__any(again)) again = choose<double, kList>(a, m, top, &mine) && again;
+  again = (again || odd) && open;
+  const bool has = m.lane16 < a.top_k && mine > kOpen;
+  const int e = index_of(mine);
+  const float l = has ? logit_at<kBf16>(row, min(e, a.experts - 1)) : -kInf;
+  float w = 0;
+  if (a.renormalize) {
+    const float largest = row_max(l);
+    if (has) {
+      if (a.sigmoid) {
+        const float t = expf(-fabsf(l));
+        w = (l > 0 ? 1.0f : expf(l - fminf(largest, 0.0f))) / (1.0f + t);
+      } else {
+        w = expf(l - largest);
+      }
+    }
+    const float total = row_add(w);
+    w = total > 0 ? w / total : w;
+  } else if (a.sigmoid) {
+    const float t = expf(-fabsf(l));
+    w = has ? (l > 0 ? 1.0f : t) / (1.0f + t) : 0.0f;
+  } else {
+    float sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) sum += Score<float>::exponential(m.x[i] - top);
+    sum = row_add(sum);
+    w = has ? expf(l - top) / sum : 0.0f;
+  }
+  if (live && !again && m.lane16 < a.top_k) {
+    a.ids[token * a.top_k + m.lane16] = has ? e : -1;
+    a.weights[token * a.top_k + m.lane16] = w * a.scale;
+  }
+  // the tokens that are still in doubt, one after the other
+  for (uint64_t left = __ballot(again && m.lane16 == 0); left; left &= left - 1) {
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 64 * 4;
+    route_exact<kBf16>(a, first + __builtin_ctzll(left) / 16, lds);
+  }
+}
+
+// ---- backward ----------------------------------------------------------------------------
 struct BackArgs {
   const float* dweights;
   const void* logits;
@@ -199,23 +610,24 @@ struct BackArgs {
   int64_t ld_out;
 };
 
+// A wave to a token, in 64 bits, for any number of choices.
 template <bool kBf16>
-__global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(BackArgs a) {
-  __shared__ float shared[kTokens][kMost];
+__global__ __launch_bounds__(kThreads) void route_backward_wave_kernel(BackArgs a) {
+  __shared__ float shared[kThreads / 64][kMost];
   float* const d = shared[threadIdx.x / 64];
   const int lane = threadIdx.x & 63;
-  const int64_t token = (int64_t)blockIdx.x * kTokens + threadIdx.x / 64;
-  const bool live = token < a.tokens;
-  const char* const row = (const char*)a.logits + (live ? token : 0) * a.ld * (kBf16 ? 2 : 4);
-  const int32_t* const ids = a.ids + (live ? token : 0) * a.top_k;
-  const float* const grads = a.dweights + (live ? token : 0) * a.top_k;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+  if (token >= a.tokens) return;
+  const char* const row = logit_row<kBf16>(a.logits, a.ld, token);
+  const int32_t* const ids = a.ids + token * a.top_k;
+  const float* const grads = a.dweights + token * a.top_k;
   const bool dense = !a.sigmoid && !a.renormalize;
   double l[kPer];
   double top = kClosed, sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     const int e = lane + 64 * i;
-    l[i] = live && e < a.experts ? (double)logit_at(row, e, kBf16) : kClosed;
+    l[i] = e < a.experts ? (double)logit_at<kBf16>(row, e) : kClosed;
     top = fmax(top, l[i]);
     d[e] = 0;
   }
@@ -227,17 +639,15 @@ __global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(BackArgs a
     sum = wave_add(sum);
     if (sum == 0) sum = 1;   // every expert is closed
   }
-  __syncthreads();
-  const auto chosen = [&](int j) {
-    const int e = live ? ids[j] : -1;
-    return e < a.experts ? e : -1;
-  };
+  wave_sync();
+  const auto chosen = [&](int j) { return ids[j] < a.experts ? ids[j] : -1; };
   double largest = kClosed;
   for (int j = lane; j < a.top_k; j += 64)
-    if (chosen(j) >= 0) largest = fmax(largest, (double)logit_at(row, chosen(j), kBf16));
+    if (chosen(j) >= 0) largest = fmax(largest, (double)logit_at<kBf16>(row, chosen(j)));
   largest = wave_max(largest);
+  if (largest == kClosed) largest = 0;   // no choice, or closed ones
   const auto weight = [&](int e) -> double {   // p, times a factor that is the same for the token where they are renormalized
-    const double v = logit_at(row, e, kBf16);
+    const double v = logit_at<kBf16>(row, e);
     if (!a.sigmoid) return a.renormalize ? exp(v - largest) : exp(v - top) / sum;
     const double m = a.renormalize ? fmin(largest, 0.0) : 0.0;
     return v > 0 ? exp(-m) / (1 + exp(-v)) : exp(v - m) / (1 + exp(v));
@@ -254,24 +664,179 @@ __global__ __launch_bounds__(64 * kTokens) void route_backward_kernel(BackArgs a
   for (int j = lane; j < a.top_k; j += 64) {
     const int e = chosen(j);
     if (e < 0) continue;
-    const double p = weight(e), v = logit_at(row, e, kBf16);
+    const double p = weight(e), v = logit_at<kBf16>(row, e);
     double h = a.renormalize ? (total != 0 ? p / total * (grads[j] - dot / total) : 0.0) : p * grads[j];
     if (a.sigmoid) h *= v > 0 ? exp(-v) / (1 + exp(-v)) : 1 / (1 + exp(v));
     atomicAdd(d + e, (float)(h * a.scale));   // one addition for each expert, unless ids names one twice
   }
-  __syncthreads();
-  if (live) {
-    char* const out = (char*)a.out + token * a.ld_out * (kBf16 ? 2 : 4);
+  wave_sync();
+  char* const out = (char*)a.out + token * a.ld_out * (kBf16 ? 2 : 4);
 #pragma unroll
-    for (int i = 0; i < kPer; i++) {
-      const int e = lane + 64 * i;
-      if (e >= a.experts) continue;
-      double v = d[e];
-      if (dense) v -= exp(l[i] - top) / sum * dot * a.scale;
-      if constexpr (kBf16) ((__bf16*)out)[e] = (__bf16)(float)v;
-      else ((float*)out)[e] = (float)v;
+  for (int i = 0; i < kPer; i++) {
+    const int e = lane + 64 * i;
+    if (e >= a.experts) continue;
+    double v = d[e];
+    if (dense) v -= exp(l[i] - top) / sum * dot * a.scale;
+    if constexpr (kBf16) ((__bf16*)out)[e] = (__bf16)(float)v;
+    else ((float*)out)[e] = (float)v;
+  }
+}
+
+// Sixteen lanes to a token, lane j with its j-th choice; the choices' gradients meet the experts' places in LDS.
+// kAt: experts that a lane reads and writes at once.
+template <int kEach, int kAt, bool kBf16>
+__global__ __launch_bounds__(kThreads) void route_backward_row_kernel(BackArgs a) {
+  keep_denormals();
+  constexpr int kRow = kEach * 16 + 4;   // the tokens' rows begin in other banks
+  __shared__ __align__(16) float shared[kThreads / 16][kRow];
+  float* const d = shared[threadIdx.x / 16];
+  const int lane16 = threadIdx.x & 15;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  const bool live = token < a.tokens;
+  const char* const row = logit_row<kBf16>(a.logits, a.ld, live ? token : 0);
+  const bool dense = !a.sigmoid && !a.renormalize;
+  const int32_t id = live && lane16 < a.top_k ? a.ids[token * a.top_k + lane16] : -1;
+  const bool has = id >= 0 && id < a.experts;
+  const float grad = has ? a.dweights[token * a.top_k + lane16] : 0.0f;
+  const float l = has ? logit_at<kBf16>(row, id) : -kInf;
+  float x[kEach], top = -kInf, sum = 1.0f;
+#pragma unroll
+  for (int i = 0; i < kEach; i++) d[i * 16 + lane16] = 0;
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < kEach; i += kAt) {
+      const int e = i * 16 + lane16 * kAt;
+      if constexpr (kAt == 1) {
+        x[i] = e < a.experts ? logit_at<kBf16>(row, e) : -kInf;
+      } else {
+        const u32x4 w = e < a.experts ? *(const u32x4*)(row + e * (kBf16 ? 2 : 4)) : u32x4{};
+#pragma unroll
+        for (int j = 0; j < kAt; j++) {
+          const uint32_t bits = kBf16 ? (j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16) : w[j % 4];
+          x[i + j] = e < a.experts ? __builtin_bit_cast(float, bits) : -kInf;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; i++) top = __builtin_elementwise_maximum(top, x[i]);
+    top = row_max(top);
+    if (top == -kInf) top = 0;
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      x[i] = __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+      sum += x[i];
+    }
+    sum = row_add(sum);
+    if (sum == 0) sum = 1;   // every expert is closed
+  }
+  float largest = row_max(l), p = 0, h = 0;
+  if (largest == -kInf) largest = 0;   // no choice, or closed ones
+  const float t = expf(-fabsf(l));
+  if (has) {   // p, times a factor that is the same for the token where they are renormalized
+    if (!a.sigmoid) p = a.renormalize ? expf(l - largest) : expf(l - top) / sum;
+    else p = (l > 0 ? 1.0f : expf(l - (a.renormalize ? fminf(largest, 0.0f) : 0.0f))) / (1.0f + t);
+  }
+  const float total = row_add(p), dot = row_add(p * grad);
+  if (has) {
+    h = a.renormalize ? (total != 0 ? p / total * (grad - dot / total) : 0.0f) : p * grad;
+    if (a.sigmoid) h *= (l > 0 ? t : 1.0f) / (1.0f + t);
+  }
+  wave_sync();   // a token's lanes are of one wave
+  if (has) atomicAdd(d + id, h * a.scale);   // one addition for each expert, unless ids names one twice
+  wave_sync();
+  if (!live) return;
+  const float less = dense ? dot * a.scale / sum : 0.0f;
+  char* const out = (char*)a.out + token * a.ld_out * (kBf16 ? 2 : 4);
+#pragma unroll
+  for (int i = 0; i < kEach; i += kAt) {
+    const int e = i * 16 + lane16 * kAt;
+    if (e >= a.experts) continue;
+    if constexpr (kAt == 1) {
+      const float v = dense ? d[e] - x[i] * less : d[e];
+      if constexpr (kBf16) ((__bf16*)out)[e] = (__bf16)v;
+      else ((float*)out)[e] = v;
+    } else {
+      f32x8 v{};
+#pragma unroll
+      for (int j = 0; j < kAt; j++) v[j] = dense ? d[e + j] - x[i + j] * less : d[e + j];
+      const Chunk<uint16_t> b = narrow<uint16_t>(v);
+      const u32x4 half{b.w[0], b.w[1], b.w[2], b.w[3]};
+      const u32x8 full = __builtin_bit_cast(u32x8, v);
+      *(u32x4*)(out + e * (kBf16 ? 2 : 4)) = kBf16 ? half : u32x4{full[0], full[1], full[2], full[3]};
     }
   }
+}
+
+// ---- host --------------------------------------------------------------------------------
+
+// Up to 2^31 lanes a launch; `from` gives the arguments from a token on.
+template <typename Args, typename From, typename Kernel>
+int launch_tokens(const Args& a, int lanes, From from, Kernel kernel, size_t lds, hipStream_t stream) {
+  const int64_t step = rows_per_launch(lanes), per = kThreads / lanes;
+  for (int64_t t = 0; t < a.tokens; t += step) {
+    Args b = from(t);
+    b.tokens = (int)std::min<int64_t>(step, a.tokens - t);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((b.tokens + per - 1) / per)), dim3(kThreads), lds, stream, b);
+    const int st = launch_status();
+    if (st != MXQ_OK) return st;
+  }
+  return MXQ_OK;
+}
+
+constexpr int kListMost = 16;   // choices of a token that sixteen lanes share
+
+template <bool kBf16>
+int launch_route(RouteArgs a, hipStream_t stream) {
+  const auto from = [&a](int64_t t) {
+    RouteArgs b = a;
+    b.logits = (const char*)a.logits + t * a.ld * (kBf16 ? 2 : 4);
+    if (a.mask) b.mask += t;
+    b.ids += t * a.top_k;
+    b.weights += t * a.top_k;
+    return b;
+  };
+  const size_t lds = kThreads / 64 * WaveLds::bytes(a.experts, a.top_k, a.groups);
+  // groups of whole lanes: 1, 2, 4, 8 or 16 of them
+  if (a.groups > 16 || (a.groups & (a.groups - 1)) || a.top_k > kListMost)
+    return launch_tokens(a, 64, from, route_wave_kernel<kBf16>, lds, stream);
+  const int size = a.experts / a.groups, lanes = 16 / a.groups;
+  a.group_lanes_log = __builtin_ctz(lanes);
+  a.per = (size + lanes - 1) / lanes;
+  constexpr int kAt = kBf16 ? 8 : 4;
+  a.wide = a.per * lanes == size && a.per % kAt == 0 && aligned(a.logits, 16) && a.ld % kAt == 0;
+  a.wide_bias = a.per * lanes == size && a.per % 4 == 0 && aligned(a.bias, 16);
+  const bool few = a.top_k <= 8;
+#define MXQ_ROUTE(kEach) \
+  return few ? launch_tokens(a, 16, from, route_row_kernel<kEach, 8, kBf16>, lds, stream) \
+             : launch_tokens(a, 16, from, route_row_kernel<kEach, 16, kBf16>, lds, stream)
+  if (a.per <= 4) MXQ_ROUTE(4);
+  if (a.per <= 8) MXQ_ROUTE(8);
+  if (a.per <= 16) MXQ_ROUTE(16);
+  MXQ_ROUTE(32);
+#undef MXQ_ROUTE
+}
+
+template <bool kBf16>
+int launch_backward(const BackArgs& a, hipStream_t stream) {
+  const auto from = [&a](int64_t t) {
+    BackArgs b = a;
+    b.dweights += t * a.top_k;
+    b.ids += t * a.top_k;
+    b.logits = (const char*)a.logits + t * a.ld * (kBf16 ? 2 : 4);
+    b.out = (char*)a.out + t * a.ld_out * (kBf16 ? 2 : 4);
+    return b;
+  };
+  if (a.top_k > kListMost) return launch_tokens(a, 64, from, route_backward_wave_kernel<kBf16>, 0, stream);
+  constexpr int kAt = kBf16 ? 8 : 4;
+  const bool wide = a.experts % kAt == 0 && aligned(a.logits, 16) && aligned(a.out, 16) && a.ld % kAt == 0 && a.ld_out % kAt == 0;
+#define MXQ_BACK(kEach) \
+  return wide ? launch_tokens(a, 16, from, route_backward_row_kernel<kEach, kAt, kBf16>, 0, stream) \
+              : launch_tokens(a, 16, from, route_backward_row_kernel<kEach, 1, kBf16>, 0, stream)
+  if (a.experts <= 128) MXQ_BACK(8);
+  if (a.experts <= 256) MXQ_BACK(16);
+  MXQ_BACK(32);
+#undef MXQ_BACK
 }
 
 int check(int64_t tokens, int64_t experts, int64_t top_k, mxq_dtype dt, int score, float scale) {
@@ -307,20 +872,10 @@ int mxq_route_experts(const void* logits, int64_t ld_logits, int64_t n_tokens, i
   if (!all_ok({rl, rb, rm, ri, rw}) || !aligned(logits, es) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
     return MXQ_ERR_SHAPE;
   if (!disjoint({ri, rw}, {rl, rb, rm})) return MXQ_ERR_ALIAS;
-  const int64_t step = rows_per_launch(64);
-  for (int64_t t = 0; t < n_tokens; t += step) {
-    const int64_t n = std::min(step, n_tokens - t);
-    const RouteArgs a{(const char*)logits + t * ld_logits * (int64_t)es, ld_logits, (int)n, (int)n_experts, bias,
-                      mask ? mask + t : mask, score == MXQ_SIGMOID, renormalize != 0, scale, (int)n_groups, (int)top_groups,
-                      (int)group_top, (int)top_k, mxq_divisor((uint32_t)(n_experts / n_groups)), ids + t * top_k,
-                      weights + t * top_k};
-    const dim3 grid((uint32_t)((n + kTokens - 1) / kTokens)), block(64 * kTokens);
-    if (dt == MXQ_BF16) hipLaunchKernelGGL((route_kernel<true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((route_kernel<false>), grid, block, 0, stream, a);
-    const int rc = launch_status();
-    if (rc != MXQ_OK) return rc;
-  }
-  return MXQ_OK;
+  const RouteArgs a{logits, ld_logits, (int)n_tokens, (int)n_experts, bias, mask, score == MXQ_SIGMOID, renormalize != 0,
+                    scale, (int)n_groups, (int)top_groups, (int)group_top, (int)top_k,
+                    mxq_divisor((uint32_t)(n_experts / n_groups)), 0, 0, false, false, ids, weights};
+  return dt == MXQ_BF16 ? launch_route<true>(a, stream) : launch_route<false>(a, stream);
 }
 
 int mxq_route_experts_backward(const float* dweights, const void* logits, int64_t ld_logits, const int32_t* ids,
@@ -338,19 +893,9 @@ int mxq_route_experts_backward(const float* dweights, const void* logits, int64_
   if (!all_ok({rg, rl, ri, rd}) || !aligned(dweights, 4) || !aligned(logits, es) || !aligned(ids, 4) || !aligned(dlogits, es))
     return MXQ_ERR_SHAPE;
   if (!disjoint({rd}, {rg, rl, ri})) return MXQ_ERR_ALIAS;
-  const int64_t step = rows_per_launch(64);
-  for (int64_t t = 0; t < n_tokens; t += step) {
-    const int64_t n = std::min(step, n_tokens - t);
-    const BackArgs a{dweights + t * top_k, (const char*)logits + t * ld_logits * (int64_t)es, ld_logits, ids + t * top_k,
-                     (int)n, (int)n_experts, (int)top_k, score == MXQ_SIGMOID, renormalize != 0, scale,
-                     (char*)dlogits + t * ld_dlogits * (int64_t)es, ld_dlogits};
-    const dim3 grid((uint32_t)((n + kTokens - 1) / kTokens)), block(64 * kTokens);
-    if (dt == MXQ_BF16) hipLaunchKernelGGL((route_backward_kernel<true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((route_backward_kernel<false>), grid, block, 0, stream, a);
-    const int rc = launch_status();
-    if (rc != MXQ_OK) return rc;
-  }
-  return MXQ_OK;
+  const BackArgs a{dweights, logits, ld_logits, ids, (int)n_tokens, (int)n_experts, (int)top_k, score == MXQ_SIGMOID,
+                   renormalize != 0, scale, dlogits, ld_dlogits};
+  return dt == MXQ_BF16 ? launch_backward<true>(a, stream) : launch_backward<false>(a, stream);
 }
 
 }  // extern "C"
