@@ -39,9 +39,9 @@ __device__ __forceinline__ Chunk<T> narrow(f32x8 f) {
   return v;
 }
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kOnce = false>
 __device__ __forceinline__ f32x8 load_floats(const void* row, int c, int K) {
-  return widen<T>(load_chunk<T, kVec>((const T*)row, c, K));
+  return widen<T>(load_chunk<T, kVec, kOnce>((const T*)row, c, K));
 }
 
 template <typename T, bool kVec, bool kStream = false>
@@ -57,6 +57,10 @@ __device__ __forceinline__ void store_floats(void* row, int c, int K, f32x8 f) {
         else ((u32x4*)p)[i] = q;
       }
     }
+  } else if (c + kEPL <= K) {
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::kWords / 4; i++)
+      reinterpret_cast<u32x4_any*>(p)[i] = u32x4{v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]};
   } else {
 #pragma unroll
     for (int i = 0; i < kEPL; i++)
@@ -83,8 +87,19 @@ __device__ __forceinline__ float add8(f32x8 v) {
 // Sum over the aligned groups of kLanes lanes of a wave, the same in each of them.
 template <int kLanes>
 __device__ __forceinline__ float lane_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < kLanes; m <<= 1) v += __shfl_xor(v, m);
+  const auto with = [](float v, uint32_t o) { return v + __builtin_bit_cast(float, o); };
+  const auto bits = [](float v) { return __builtin_bit_cast(uint32_t, v); };
+  v = with(v, dpp<0xB1>(bits(v)));    // quad_perm [1,0,3,2]
+  v = with(v, dpp<0x4E>(bits(v)));    // quad_perm [2,3,0,1]
+  v = with(v, dpp<0x141>(bits(v)));   // row_half_mirror: quads hold one value each by now
+  v = with(v, dpp<0x140>(bits(v)));   // row_mirror
+  static_assert(kLanes == 16 || kLanes == 64, "a row of lanes or a wave");
+  if constexpr (kLanes == 64) {
+    u32x2 s = swap16(bits(v), bits(v));
+    v = __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
+    s = swap32(bits(v), bits(v));
+    v = __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
+  }
   return v;
 }
 

@@ -86,24 +86,30 @@ __device__ __forceinline__ uint32_t code_of(uint32_t amax) {
   return amax >= kInf ? 255u : (uint32_t)max(code, 0);
 }
 
-// Elements [c, c + 8) of a row of K; those from K on are 0.  kOnce: with the non-temporal hint, for rows that nothing
-// reads again soon.
+// The same 16 and 8 bytes at any address: the hardware's loads and stores take them.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// Elements [c, c + 8) of a row of K; those from K on are 0.  kVec: rows lie at multiples of 16 bytes and K is a multiple of 8.
+// kOnce: with the non-temporal hint, for rows that nothing reads again soon.
 template <typename T, bool kVec, bool kOnce = false>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int K) {
   Chunk<T> v;
-  if (kVec) {
-    if (c < K) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(row + c);
+  if (kVec ? c < K : c + kEPL <= K) {
 #pragma unroll
-      for (int i = 0; i < Chunk<T>::kWords / 4; i++)
-        reinterpret_cast<u32x4*>(v.w)[i] = kOnce ? __builtin_nontemporal_load(p + i) : p[i];
-      return v;
+    for (int i = 0; i < Chunk<T>::kWords / 4; i++) {
+      if constexpr (kVec) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(row + c) + i;
+        reinterpret_cast<u32x4*>(v.w)[i] = kOnce ? __builtin_nontemporal_load(p) : *p;
+      } else {
+        reinterpret_cast<u32x4*>(v.w)[i] = reinterpret_cast<const u32x4_any*>(row + c)[i];
+      }
     }
+    return v;
+  }
 #pragma unroll
-    for (int i = 0; i < Chunk<T>::kWords; i++) v.w[i] = 0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < Chunk<T>::kWords; i++) v.w[i] = 0;
+  for (int i = 0; i < Chunk<T>::kWords; i++) v.w[i] = 0;
+  if (!kVec && c < K) {   // the end of the row
 #pragma unroll
     for (int i = 0; i < kEPL; i++)
       if (c + i < K) {
@@ -121,6 +127,8 @@ __device__ __forceinline__ void store_chunk(uint8_t* row, int c, int K, u32x2 v)
       if (kStream) __builtin_nontemporal_store(v, reinterpret_cast<u32x2*>(row + c));
       else *reinterpret_cast<u32x2*>(row + c) = v;
     }
+  } else if (c + kEPL <= K) {
+    *reinterpret_cast<u32x2_any*>(row + c) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < kEPL; i++)

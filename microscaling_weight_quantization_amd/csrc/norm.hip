@@ -20,12 +20,6 @@ namespace {
 using namespace mxq_host;
 using namespace mxq_dev;
 
-// What a row's values are multiplied by: s * r, then * f (the other way round small values of a row of huge ones
-// would vanish on the way).  f is 1 but for rows whose squares overflow.
-struct Stats {
-  float f, r;
-};
-
 struct NormArgs {
   const void *x, *residual, *weight;
   int64_t ld_x, ld_res;
@@ -36,7 +30,7 @@ struct NormArgs {
   int64_t ld_sum, ld_y;
   uint8_t *data, *scale;
   int64_t ld_data, scale_ld;
-  Stats* stats;
+  float* stats;   // 1 / sqrt(mean(s^2) + eps) of each row
 };
 
 constexpr float kDown = 0x1p-80f;
@@ -56,33 +50,46 @@ __device__ __forceinline__ f32x8 stream_at(const NormArgs& a, int64_t row, int c
   return widen<TS>(narrow<TS>(x + r));
 }
 
-// Sum over the kLanes lanes of a row, the same in each of them; several waves of a row meet in LDS.
+// Sum over the kLanes lanes of a row, the same in each of them; several waves of a row meet in `part`, which holds 0 in the
+// places of waves that there are not, and which one sum uses.
+struct Meeting {
+  float part[16];
+};
 template <int kLanes>
-__device__ __forceinline__ float row_sum(float v, float* part) {
+__device__ __forceinline__ float row_sum(float v, Meeting& m) {
   if constexpr (kLanes <= 64) return lane_sum<kLanes>(v);
+  constexpr int kWaves = kLanes / 64;
   v = lane_sum<64>(v);
+  if ((threadIdx.x & 63) == 0) m.part[threadIdx.x / 64] = v;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = v;
-  __syncthreads();
-  float s = part[0];
-#pragma unroll
-  for (int i = 1; i < kLanes / 64; i++) s += part[i];
-  return s;
+  const int lane16 = threadIdx.x & 15;
+  return lane_sum<16>(lane16 < kWaves ? m.part[lane16] : 0.0f);
 }
 
-__device__ __forceinline__ float inverse_root(float sum, float f, const NormArgs& a) {
-  return 1.0f / sqrtf(sum / (float)a.K + a.eps * f * f);
+__device__ __forceinline__ float add_squares(f32x8 s, float sum) {
+#pragma unroll
+  for (int i = 0; i < kEPL; i++) sum = fmaf(s[i], s[i], sum);
+  return sum;
+}
+
+// r of a row from its sum of squares, or with f from that of its values times f.  f is a power of two, so r f is as exact as
+// r, but for rows beyond 2^126, whose r f has 21 places or more.
+__device__ __forceinline__ float inverse_root(float sum, float f, float eps, int K) {
+  return f / sqrtf(sum / (float)K + eps * f * f);
 }
 
 constexpr int kThreads = 256;
+// A workgroup: one row, or 256 lanes of those that are a wave's or less.
+template <int kLanes>
+constexpr int kNormThreads = kLanes > 64 ? kLanes : kThreads;
 
-// A row in the registers of kLanes lanes, kChunks pieces of eight elements each.
-template <typename TX, typename TS, int kLanes, int kChunks, bool kVec>
-__global__ __launch_bounds__(kLanes > kThreads ? kLanes : kThreads) void norm_kernel(NormArgs a) {
+// A row in the registers of kLanes lanes, kChunks pieces of eight elements each.  kStream: outputs leave with the
+// non-temporal hint.
+template <typename TX, typename TS, int kLanes, int kChunks, bool kVec, bool kStream>
+__global__ __launch_bounds__(kNormThreads<kLanes>) void norm_kernel(NormArgs a) {
   keep_denormals();
-  constexpr int kRows = kLanes < kThreads ? kThreads / kLanes : 1;
-  __shared__ float part[16];
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
+  __shared__ Meeting meet[2];
+  const int64_t row = (int64_t)blockIdx.x * (kNormThreads<kLanes> / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
   if (row >= a.rows) return;   // a workgroup that meets at barriers has one row
   f32x8 s[kChunks];
@@ -93,25 +100,26 @@ __global__ __launch_bounds__(kLanes > kThreads ? kLanes : kThreads) void norm_ke
     s[i] = stream_at<TX, TS, kVec>(a, row, c);
   }
 #pragma unroll
-  for (int i = 0; i < kChunks; i++) sum += add8(s[i] * s[i]);
-  Stats t{1.0f, 0.0f};
-  sum = row_sum<kLanes>(sum, part);
+  for (int i = 0; i < kChunks; i++) sum = add_squares(s[i], sum);
+  sum = row_sum<kLanes>(sum, meet[0]);
+  float f = 1.0f;
   if (!(sum < __builtin_inff())) {   // the same for the whole row
-    t.f = kDown;
+    f = kDown;
     sum = 0;
 #pragma unroll
-    for (int i = 0; i < kChunks; i++) sum += add8((s[i] * kDown) * (s[i] * kDown));
-    sum = row_sum<kLanes>(sum, part);
+    for (int i = 0; i < kChunks; i++) sum = add_squares(s[i] * kDown, sum);
+    sum = row_sum<kLanes>(sum, meet[1]);
   }
-  t.r = inverse_root(sum, t.f, a);
-  if (a.stats && lane == 0) a.stats[row] = t;
+  const float r = inverse_root(sum, f, a.eps, a.K);
+  if (a.stats && lane == 0) a.stats[row] = r;
 #pragma unroll
   for (int i = 0; i < kChunks; i++) {
     const int c = (i * kLanes + lane) * kEPL;
-    const f32x8 y = s[i] * t.r * t.f * weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
-    if (a.sum) store_floats<TS, kVec>((TS*)a.sum + row * a.ld_sum, c, a.K, s[i]);
-    if (a.y) store_floats<TX, kVec>((TX*)a.y + row * a.ld_y, c, a.K, y);
-    if (a.data) store_group<kVec, false>(a.data + row * a.ld_data, a.scale + row * a.scale_ld, c, a.K, y);
+    const f32x8 y = s[i] * r * weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
+    // two stores of fp32 each fill half of a line, and the hint sends the halves out one by one: 8192 x 8192 fp32 210 -> 256 us
+    if (a.sum) store_floats<TS, kVec, kStream && sizeof(TS) == 2>((TS*)a.sum + row * a.ld_sum, c, a.K, s[i]);
+    if (a.y) store_floats<TX, kVec, kStream && sizeof(TX) == 2>((TX*)a.y + row * a.ld_y, c, a.K, y);
+    if (a.data) store_group<kVec, kStream>(a.data + row * a.ld_data, a.scale + row * a.scale_ld, c, a.K, y);
   }
 }
 
@@ -121,35 +129,32 @@ constexpr int kLong = 1024;
 template <typename TX, typename TS, bool kVec>
 __global__ __launch_bounds__(kLong) void norm_long_kernel(NormArgs a) {
   keep_denormals();
-  __shared__ float part[16];
+  __shared__ Meeting meet[2];
   const int64_t row = blockIdx.x;
   TS* const stored = a.sum ? (TS*)a.sum + row * a.ld_sum : nullptr;
   float sum = 0;
   for (int64_t c = threadIdx.x * kEPL; c < a.K; c += kLong * kEPL) {
     const f32x8 s = stream_at<TX, TS, kVec>(a, row, (int)c);
     if (stored) store_floats<TS, kVec>(stored, (int)c, a.K, s);   // the residual may be stored in its own place
-    sum += add8(s * s);
+    sum = add_squares(s, sum);
   }
   const auto again = [&](int c) {
     return stored ? load_floats<TS, kVec>(stored, c, a.K) : stream_at<TX, TS, kVec>(a, row, c);
   };
-  Stats t{1.0f, 0.0f};
-  sum = row_sum<kLong>(sum, part);
+  sum = row_sum<kLong>(sum, meet[0]);
+  float f = 1.0f;
   if (!(sum < __builtin_inff())) {
-    t.f = kDown;
+    f = kDown;
     sum = 0;
-    for (int64_t c = threadIdx.x * kEPL; c < a.K; c += kLong * kEPL) {
-      const f32x8 s = again((int)c) * kDown;
-      sum += add8(s * s);
-    }
-    sum = row_sum<kLong>(sum, part);
+    for (int64_t c = threadIdx.x * kEPL; c < a.K; c += kLong * kEPL) sum = add_squares(again((int)c) * kDown, sum);
+    sum = row_sum<kLong>(sum, meet[1]);
   }
-  t.r = inverse_root(sum, t.f, a);
-  if (a.stats && threadIdx.x == 0) a.stats[row] = t;
+  const float r = inverse_root(sum, f, a.eps, a.K);
+  if (a.stats && threadIdx.x == 0) a.stats[row] = r;
   // all lanes of a group of 16 walk as far
   for (int64_t c0 = (threadIdx.x & ~15) * kEPL; c0 < a.K; c0 += kLong * kEPL) {
     const int c = (int)c0 + (threadIdx.x & 15) * kEPL;
-    const f32x8 y = again(c) * t.r * t.f * weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
+    const f32x8 y = again(c) * r * weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
     if (a.y) store_floats<TX, kVec>((TX*)a.y + row * a.ld_y, c, a.K, y);
     if (a.data) store_group<kVec, false>(a.data + row * a.ld_data, a.scale + row * a.scale_ld, c, a.K, y);
   }
@@ -168,12 +173,12 @@ __global__ __launch_bounds__(kTileThreads) void norm_columns_kernel(NormArgs a, 
   for (int i = 0; i < kTileRows; i++) {
     const int64_t r = t.first + threadIdx.x / 16 + 16 * i;
     f32x8 s{};
-    Stats st{};
+    float root = 0;
     if (r < a.rows) {
       s = a.sum ? load_floats<TS, kVec>((const TS*)a.sum + r * a.ld_sum, c, a.K) : stream_at<TX, TS, kVec>(a, r, c);
-      st = a.stats[r];
+      root = a.stats[r];
     }
-    v[i] = narrow<uint32_t>(s * st.r * st.f * w);
+    v[i] = narrow<uint32_t>(s * root * w);
   }
   if (kVec && whole_tile(t, blockIdx.x, a.K)) store_tile<uint32_t, kVec, false, kStream, kVec>(v, out, t, id, blockIdx.x, shared);
   else store_tile<uint32_t, kVec, false, kStream, false>(v, out, t, id, blockIdx.x, shared);
@@ -185,36 +190,162 @@ struct BackArgs {
   int64_t ld_dy, ld_s, ld_dres;
   bool w_bf16;
   float eps;
-  int rows, K, per_block;   // rows of a block of the second kernel
+  int rows, K, per_block;   // rows of a workgroup (of a block, where rows are long)
   void* dx;
   int64_t ld_dx;
-  float4* stats;            // f, r, mean(g u) of each row
+  float2* stats;            // r and mean(g u) of each row, where rows are long
   float* part;              // [blocks, K] sums of dw; null: not wanted
 };
+
+// What a lane reads of a row.
+template <typename TY, typename TS, int kChunks>
+struct BackRow {
+  Chunk<TS> s[kChunks], dres[kChunks];
+  Chunk<TY> dy[kChunks];
+};
+
+// A workgroup takes per_block rows one after the other (as many at a time as it has lanes for), the next row on its way while
+// this one is worked out, and keeps its part of dw in registers.  Loads with the non-temporal hint, stores without: 8192 x 8192
+// bf16 99.9 us, plain loads 113, stores with it as well 102.5, loads without and stores with it 109.
+template <typename TY, typename TS, int kLanes, int kChunks, bool kVec>
+__global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) {
+  keep_denormals();
+  constexpr int kSlots = kNormThreads<kLanes> / kLanes, kWaves = kLanes / 64;
+  __shared__ float2 meet[2][16];
+  __shared__ float fold[kSlots > 1 ? kSlots : 1][kSlots > 1 ? kLanes * kEPL : 1];
+  const int slot = kSlots > 1 ? threadIdx.x / kLanes : 0, lane = threadIdx.x % kLanes;
+  const int64_t lo = (int64_t)blockIdx.x * a.per_block, hi = min(lo + a.per_block, (int64_t)a.rows);
+  f32x8 w[kChunks], dw[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; i++) {
+    w[i] = weight_at<kVec>(a.weight, a.w_bf16, (i * kLanes + lane) * kEPL, a.K);
+    dw[i] = f32x8{};
+  }
+  using Row = BackRow<TY, TS, kChunks>;
+  const auto load = [&](Row& v, int64_t row) {
+    const int64_t r = min(row, (int64_t)a.rows - 1);
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) {
+      const int c = row < hi ? (i * kLanes + lane) * kEPL : a.K;
+      v.s[i] = load_chunk<TS, kVec, true>((const TS*)a.s + r * a.ld_s, c, a.K);
+      v.dy[i] = load_chunk<TY, kVec, true>((const TY*)a.dy + r * a.ld_dy, c, a.K);
+      if (a.dres) v.dres[i] = load_chunk<TS, kVec, true>((const TS*)a.dres + r * a.ld_dres, c, a.K);
+    }
+  };
+  int turn = 0;
+  // (sum of squares, sum of g s) of a row from its lanes' parts, the same in all of them
+  const auto meeting = [&](float2 v) {
+    v = float2{lane_sum<kLanes == 16 ? 16 : 64>(v.x), lane_sum<kLanes == 16 ? 16 : 64>(v.y)};
+    if constexpr (kLanes > 64) {   // the waves meet in one of two places in turn, so that one barrier is enough
+      if ((threadIdx.x & 63) == 0) meet[turn][threadIdx.x / 64] = v;
+      __syncthreads();
+      const int lane16 = threadIdx.x & 15;
+      v = lane16 < kWaves ? meet[turn][lane16] : float2{0, 0};
+      v = float2{lane_sum<16>(v.x), lane_sum<16>(v.y)};
+      turn ^= 1;
+    }
+    return v;
+  };
+  const auto work = [&](const Row& v, int64_t row) {
+    float2 sum{0, 0};
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) {
+      const f32x8 s = widen<TS>(v.s[i]), g = widen<TY>(v.dy[i]) * w[i];
+#pragma unroll
+      for (int j = 0; j < kEPL; j++) sum.x = fmaf(s[j], s[j], sum.x), sum.y = fmaf(g[j], s[j], sum.y);
+    }
+    sum = meeting(sum);
+    float f = 1.0f;
+    if (!(sum.x < __builtin_inff())) {   // the same for the whole row
+      f = kDown;
+      sum = float2{0, 0};
+#pragma unroll
+      for (int i = 0; i < kChunks; i++) {
+        const f32x8 s = widen<TS>(v.s[i]) * kDown, g = widen<TY>(v.dy[i]) * w[i];
+        sum.x = add_squares(s, sum.x);
+        sum.y += add8(g * s);
+      }
+      sum = meeting(sum);
+    }
+    const float r = inverse_root(sum.x, f, a.eps, a.K), m = sum.y * (r / f) / (float)a.K;
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) {
+      const int c = row < hi ? (i * kLanes + lane) * kEPL : a.K;
+      const f32x8 u = widen<TS>(v.s[i]) * r, dy = widen<TY>(v.dy[i]);
+      f32x8 dx = a.dres ? widen<TS>(v.dres[i]) : f32x8{};
+#pragma unroll
+      for (int j = 0; j < kEPL; j++) {
+        dx[j] = fmaf(fmaf(-u[j], m, dy[j] * w[i][j]), r, dx[j]);
+        dw[i][j] = fmaf(dy[j], u[j], dw[i][j]);
+      }
+      store_floats<TS, kVec>((TS*)a.dx + row * a.ld_dx, c, a.K, dx);
+    }
+  };
+  Row even;
+  if constexpr (kChunks > 1) {   // two rows of these would not fit into the registers
+    for (int64_t row = lo + slot; row - slot < hi; row += kSlots) {
+      load(even, row);
+      work(even, row);
+    }
+  } else {
+    Row odd;
+    load(even, lo + slot);
+    for (int64_t row = lo + slot; row - slot < hi; row += 2 * kSlots) {
+      load(odd, row + kSlots);
+      work(even, row);
+      if (row - slot + kSlots >= hi) break;
+      load(even, row + 2 * kSlots);
+      work(odd, row + kSlots);
+    }
+  }
+  if (!a.part) return;   // the same for all
+  float* const p = a.part + (int64_t)blockIdx.x * a.K;
+  if constexpr (kSlots > 1) {
+#pragma unroll
+    for (int i = 0; i < kEPL; i++) fold[slot][lane * kEPL + i] = dw[0][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.K; c += kNormThreads<kLanes>) {   // K is at most kLanes * 8
+      float sum = fold[0][c];
+#pragma unroll
+      for (int i = 1; i < kSlots; i++) sum += fold[i][c];
+      p[c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) {
+      const int c = (i * kLanes + lane) * kEPL;
+#pragma unroll
+      for (int j = 0; j < kEPL; j++)
+        if (c + j < a.K) p[c + j] = dw[i][j];
+    }
+  }
+}
+
+// Rows that the registers do not hold: their statistics first, then dx and the parts of dw, a column a lane.
 
 template <typename TY, typename TS, bool kVec>
 __global__ __launch_bounds__(kThreads) void back_stats_kernel(BackArgs a) {
   keep_denormals();
-  __shared__ float part[16];
+  __shared__ Meeting meet[4];
   const int64_t row = blockIdx.x;
   const TS* const s = (const TS*)a.s + row * a.ld_s;
   const TY* const dy = (const TY*)a.dy + row * a.ld_dy;
   float f = 1.0f, sum, dot;
-  for (;;) {
+  for (int k = 0;; k += 2) {
     sum = dot = 0;
     for (int64_t c = threadIdx.x * kEPL; c < a.K; c += kThreads * kEPL) {
       const f32x8 v = load_floats<TS, kVec>(s, (int)c, a.K) * f;
       const f32x8 g = load_floats<TY, kVec>(dy, (int)c, a.K) * weight_at<kVec>(a.weight, a.w_bf16, (int)c, a.K);
-      sum += add8(v * v);
+      sum = add_squares(v, sum);
       dot += add8(g * v);
     }
-    sum = row_sum<kThreads>(sum, part);
-    dot = row_sum<kThreads>(dot, part);
-    if (sum < __builtin_inff() || f != 1.0f) break;
+    sum = row_sum<kThreads>(sum, meet[k]);
+    dot = row_sum<kThreads>(dot, meet[k + 1]);
+    if (sum < __builtin_inff() || k) break;   // the same for all
     f = kDown;
   }
-  const float r = 1.0f / sqrtf(sum / (float)a.K + a.eps * f * f);
-  if (threadIdx.x == 0) a.stats[row] = float4{f, r, dot * r / (float)a.K, 0.0f};
+  const float r = inverse_root(sum, f, a.eps, a.K);
+  if (threadIdx.x == 0) a.stats[row] = float2{r, dot * (r / f) / (float)a.K};
 }
 
 // dx of a block of rows and 2048 columns, and its part of dw.
@@ -229,10 +360,10 @@ __global__ __launch_bounds__(kThreads) void back_rows_kernel(BackArgs a) {
   const f32x8 w = weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
   f32x8 dw{};
   for (int64_t row = lo; row < hi; row++) {
-    const float4 t = a.stats[row];
-    const f32x8 u = load_floats<TS, kVec>((const TS*)a.s + row * a.ld_s, c, a.K) * t.y * t.x;
+    const float2 t = a.stats[row];
+    const f32x8 u = load_floats<TS, kVec>((const TS*)a.s + row * a.ld_s, c, a.K) * t.x;
     const f32x8 dy = load_floats<TY, kVec>((const TY*)a.dy + row * a.ld_dy, c, a.K);
-    f32x8 dx = (dy * w - u * t.z) * t.y * t.x;
+    f32x8 dx = (dy * w - u * t.y) * t.x;
     if (a.dres) dx += load_floats<TS, kVec>((const TS*)a.dres + row * a.ld_dres, c, a.K);
     store_floats<TS, kVec>((TS*)a.dx + row * a.ld_dx, c, a.K, dx);
     dw += dy * u;
@@ -245,20 +376,23 @@ __global__ __launch_bounds__(kThreads) void back_rows_kernel(BackArgs a) {
   }
 }
 
-// dw: the blocks' parts added up in their order, 64 columns a workgroup, its 16 waves taking turns.
-constexpr int kFoldThreads = 1024;
-__global__ __launch_bounds__(kFoldThreads) void back_weight_kernel(const float* part, int blocks, int K, float* dw) {
-  __shared__ float sums[kFoldThreads / 64][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-  const int c = blockIdx.x * 64 + lane;
+// dw: the blocks' parts added up in an order that their number fixes, 32 columns a workgroup, 32 of its lanes a column.
+constexpr int kFoldThreads = 1024, kFoldColumns = 32, kFoldSlots = kFoldThreads / kFoldColumns;
+__global__ __launch_bounds__(kFoldThreads) void back_weight_kernel(const float* part, int blocks, int K, int first,
+                                                                   float* dw) {
+  __shared__ float sums[kFoldSlots][kFoldColumns + 1];
+  const int lane = threadIdx.x % kFoldColumns, slot = threadIdx.x / kFoldColumns;
+  const int64_t c = first + (int64_t)blockIdx.x * kFoldColumns + lane;
   float sum = 0;
-  if (c < K)
-    for (int b = wave; b < blocks; b += kFoldThreads / 64) sum += part[(int64_t)b * K + c];
-  sums[wave][lane] = sum;
+  if (c < K) {
+#pragma unroll 4
+    for (int b = slot; b < blocks; b += kFoldSlots) sum += part[(int64_t)b * K + c];
+  }
+  sums[slot][lane] = sum;
   __syncthreads();
-  if (wave == 0 && c < K) {
+  if (slot == 0 && c < K) {
 #pragma unroll
-    for (int i = 1; i < kFoldThreads / 64; i++) sum += sums[i][lane];
+    for (int i = 1; i < kFoldSlots; i++) sum += sums[i][lane];
     dw[c] = sum;
   }
 }
@@ -284,29 +418,32 @@ NormArgs from_row(NormArgs a, int64_t r, int64_t n) {
   return a;
 }
 
-template <typename TX, typename TS, int kLanes, int kChunks, bool kVec>
+template <typename TX, typename TS, int kLanes, int kChunks, bool kVec, bool kStream>
 int launch_norm(const NormArgs& a, hipStream_t stream) {
-  constexpr int threads = std::max(kLanes, kThreads), per = threads / kLanes;
+  constexpr int threads = kNormThreads<kLanes>, per = threads / kLanes;
   const int64_t step = rows_per_launch(kLanes);
   for (int64_t r = 0; r < a.rows; r += step) {
     const int64_t n = std::min<int64_t>(step, a.rows - r);
-    hipLaunchKernelGGL((norm_kernel<TX, TS, kLanes, kChunks, kVec>), dim3((uint32_t)((n + per - 1) / per)), dim3(threads),
-                       0, stream, from_row<TX, TS>(a, r, n));
+    hipLaunchKernelGGL((norm_kernel<TX, TS, kLanes, kChunks, kVec, kStream>), dim3((uint32_t)((n + per - 1) / per)),
+                       dim3(threads), 0, stream, from_row<TX, TS>(a, r, n));
     MXQ_TRY(launch_status());
   }
   return MXQ_OK;
 }
 
-// A row takes as many lanes as hold it in up to eight pieces each.
-template <typename TX, typename TS, bool kVec>
+// A row takes as many lanes as hold it in one piece each, up to a workgroup of 1024 with two: 8192 x 8192 bf16 with a
+// residual and y 106 us, with 512 lanes and two pieces 112, with 256 and four 120.
+template <typename TX, typename TS, bool kVec, bool kStream>
 int norm_rows(const NormArgs& a, hipStream_t stream) {
   const int K = a.K;
-  if (K <= 16 * 8) return launch_norm<TX, TS, 16, 1, kVec>(a, stream);
-  if (K <= 64 * 8) return launch_norm<TX, TS, 64, 1, kVec>(a, stream);
-  if (K <= 256 * 8) return launch_norm<TX, TS, 256, 1, kVec>(a, stream);
-  if (K <= 256 * 16) return launch_norm<TX, TS, 256, 2, kVec>(a, stream);
-  if (K <= 256 * 32) return launch_norm<TX, TS, 256, 4, kVec>(a, stream);
-  if (K <= 1024 * 16) return launch_norm<TX, TS, 1024, 2, kVec>(a, stream);
+  if (K <= 16 * 8) return launch_norm<TX, TS, 16, 1, kVec, kStream>(a, stream);
+  if (K <= 64 * 8) return launch_norm<TX, TS, 64, 1, kVec, kStream>(a, stream);
+  if (K <= 128 * 8) return launch_norm<TX, TS, 128, 1, kVec, kStream>(a, stream);
+  if (K <= 256 * 8) return launch_norm<TX, TS, 256, 1, kVec, kStream>(a, stream);
+  if (K <= 512 * 8) return launch_norm<TX, TS, 512, 1, kVec, kStream>(a, stream);
+  if (K <= 768 * 8) return launch_norm<TX, TS, 768, 1, kVec, kStream>(a, stream);
+  if (K <= 1024 * 8) return launch_norm<TX, TS, 1024, 1, kVec, kStream>(a, stream);
+  if (K <= 1024 * 16) return launch_norm<TX, TS, 1024, 2, kVec, kStream>(a, stream);
   const int64_t step = rows_per_launch(kLong);
   for (int64_t r = 0; r < a.rows; r += step) {
     const int64_t n = std::min<int64_t>(step, a.rows - r);
@@ -334,7 +471,11 @@ int norm_columns(const NormArgs& a, const TileOut& out, bool vec, hipStream_t st
 
 template <typename TX, typename TS>
 int norm_launch(const NormArgs& a, const TileOut* columns, bool vec, hipStream_t stream) {
-  MXQ_TRY(vec ? (norm_rows<TX, TS, true>(a, stream)) : (norm_rows<TX, TS, false>(a, stream)));
+  // The hint for outputs that nothing reads at once: not for a sum that the columns come from.  8192 x 8192 bf16 106 ->
+  // 102 us, 2048 x 8192 27.4 -> 22.9; rows and columns of 4096 x 8192 with the hint 92.8 -> 99.0.
+  MXQ_TRY(!vec      ? (norm_rows<TX, TS, false, false>(a, stream))
+          : columns ? (norm_rows<TX, TS, true, false>(a, stream))
+                    : (norm_rows<TX, TS, true, true>(a, stream)));
   return columns ? norm_columns<TX, TS>(a, *columns, vec, stream) : MXQ_OK;
 }
 
@@ -380,7 +521,7 @@ int norm_entry(const void* x, int64_t ld_x, const void* residual, int64_t ld_res
                    (!col || wide_payload(col->data, col->ld));
   const NormArgs a{x,   residual, weight, ld_x, ld_res, w_dt == MXQ_BF16,     eps,   (int)rows, (int)K,
                    sum, y,        ld_sum, ld_y, fp8 ? data : nullptr, scale, ld_data, scale_ld,
-                   col ? (Stats*)col->workspace : nullptr};
+                   col ? (float*)col->workspace : nullptr};
   TileOut out{};
   if (col)
     out = TileOut{(int)K, (int)groups_of(rows), nullptr, 0, nullptr, 0, col->data, col->ld, col->scale, col->scale_ld};
@@ -392,16 +533,42 @@ int norm_entry(const void* x, int64_t ld_x, const void* residual, int64_t ld_res
                             : norm_launch<uint32_t, uint32_t>(a, o, vec, stream);
 }
 
-// Rows of a block of the backward pass: enough blocks to fill the card, few enough that their parts stay small.
-int64_t back_rows_per_block(int64_t rows) { return std::max<int64_t>(4, (rows + 255) / 256); }
-int64_t back_blocks(int64_t rows) {
-  const int64_t per = back_rows_per_block(rows);
+constexpr int kHeld = 1024 * 16;   // elements of a row that registers hold
+// Lanes of a workgroup of the backward pass.
+int back_threads(int64_t K) {
+  for (int lanes : {64, 128, 256, 512, 768})
+    if (K <= lanes * 8) return lanes > 64 ? lanes : kThreads;
+  return 1024;
+}
+// Rows of a workgroup: as many workgroups as have 1024 lanes for each CU (8192 x 8192 bf16 108.5 us; twice as many 115).
+int64_t back_rows_per_block(int64_t rows, int64_t K) {
+  const int64_t fill = K > kHeld ? 256 : 256 * 1024 / back_threads(K);
+  return std::max<int64_t>(K > kHeld ? 4 : 1, (rows + fill - 1) / fill);
+}
+int64_t back_blocks(int64_t rows, int64_t K) {
+  const int64_t per = back_rows_per_block(rows, K);
   return (rows + per - 1) / per;
 }
 
+template <typename TY, typename TS, int kLanes, int kChunks, bool kVec>
+int launch_back(const BackArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((back_kernel<TY, TS, kLanes, kChunks, kVec>), dim3((uint32_t)back_blocks(a.rows, a.K)),
+                     dim3(kNormThreads<kLanes>), 0, stream, a);
+  return launch_status();
+}
+
 template <typename TY, typename TS, bool kVec>
-int back_launch(BackArgs a, float* dw, hipStream_t stream) {
-  const int64_t step = rows_per_launch(kThreads), blocks = back_blocks(a.rows);
+int back_rows(const BackArgs& a, hipStream_t stream) {
+  const int K = a.K;
+  if (K <= 16 * 8) return launch_back<TY, TS, 16, 1, kVec>(a, stream);
+  if (K <= 64 * 8) return launch_back<TY, TS, 64, 1, kVec>(a, stream);
+  if (K <= 128 * 8) return launch_back<TY, TS, 128, 1, kVec>(a, stream);
+  if (K <= 256 * 8) return launch_back<TY, TS, 256, 1, kVec>(a, stream);
+  if (K <= 512 * 8) return launch_back<TY, TS, 512, 1, kVec>(a, stream);
+  if (K <= 768 * 8) return launch_back<TY, TS, 768, 1, kVec>(a, stream);
+  if (K <= 1024 * 8) return launch_back<TY, TS, 1024, 1, kVec>(a, stream);
+  if (K <= kHeld) return launch_back<TY, TS, 1024, 2, kVec>(a, stream);
+  const int64_t step = rows_per_launch(kThreads);
   for (int64_t r = 0; r < a.rows; r += step) {
     BackArgs b = a;
     b.s = (const TS*)a.s + r * a.ld_s;
@@ -411,18 +578,26 @@ int back_launch(BackArgs a, float* dw, hipStream_t stream) {
                        dim3(kThreads), 0, stream, b);
     MXQ_TRY(launch_status());
   }
-  const uint32_t strips = (uint32_t)((a.K + kThreads * kEPL - 1) / (kThreads * kEPL));
-  hipLaunchKernelGGL((back_rows_kernel<TY, TS, kVec>), dim3(strips, (uint32_t)blocks), dim3(kThreads), 0, stream, a);
-  MXQ_TRY(launch_status());
-  if (!dw) return MXQ_OK;
-  hipLaunchKernelGGL(back_weight_kernel, dim3((uint32_t)((a.K + 63) / 64)), dim3(kFoldThreads), 0, stream, a.part,
-                     (int)blocks, a.K, dw);
+  const uint32_t strips = (uint32_t)((a.K + (int64_t)kThreads * kEPL - 1) / (kThreads * kEPL));
+  hipLaunchKernelGGL((back_rows_kernel<TY, TS, kVec>), dim3(strips, (uint32_t)back_blocks(a.rows, a.K)), dim3(kThreads), 0,
+                     stream, a);
   return launch_status();
 }
 
+int fold_weight(const float* part, int64_t blocks, int64_t K, float* dw, hipStream_t stream) {
+  const int64_t step = rows_per_launch(kFoldThreads) * kFoldColumns;
+  for (int64_t c = 0; c < K; c += step) {
+    const int64_t n = std::min(step, K - c);
+    hipLaunchKernelGGL(back_weight_kernel, dim3((uint32_t)((n + kFoldColumns - 1) / kFoldColumns)), dim3(kFoldThreads), 0,
+                       stream, part, (int)blocks, (int)K, (int)c, dw);
+    MXQ_TRY(launch_status());
+  }
+  return MXQ_OK;
+}
+
 template <typename TY, typename TS>
-int back_launch(const BackArgs& a, bool vec, float* dw, hipStream_t stream) {
-  return vec ? back_launch<TY, TS, true>(a, dw, stream) : back_launch<TY, TS, false>(a, dw, stream);
+int back_launch(const BackArgs& a, bool vec, hipStream_t stream) {
+  return vec ? back_rows<TY, TS, true>(a, stream) : back_rows<TY, TS, false>(a, stream);
 }
 
 }  // namespace
@@ -445,7 +620,7 @@ int mxq_rms_norm_fp8_group128(const void* x, int64_t ld_x, const void* residual,
 }
 
 int64_t mxq_rms_norm_fp8_group128_row_col_workspace(int64_t rows) {
-  return rows < 1 || rows > kMaxDim ? 0 : rows * (int64_t)sizeof(Stats);
+  return rows < 1 || rows > kMaxDim ? 0 : rows * 8;
 }
 
 int mxq_rms_norm_fp8_group128_row_col(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
@@ -462,7 +637,7 @@ int mxq_rms_norm_fp8_group128_row_col(const void* x, int64_t ld_x, const void* r
 
 int64_t mxq_rms_norm_backward_workspace(int64_t rows, int64_t K) {
   if (rows < 1 || K < 1 || rows > kMaxDim || K > kMaxDim) return 0;
-  return rows * 16 + back_blocks(rows) * K * 4;
+  return (K > kHeld ? rows * (int64_t)sizeof(float2) : 0) + back_blocks(rows, K) * K * 4;
 }
 
 int mxq_rms_norm_backward(const void* dy, int64_t ld_dy, mxq_dtype dt, const void* x, int64_t ld_x, mxq_dtype x_dt,
@@ -489,20 +664,20 @@ int mxq_rms_norm_backward(const void* dy, int64_t ld_dy, mxq_dtype dt, const voi
   if (!disjoint({rd, rv, wk}, {rg, rx, rw, rr})) return MXQ_ERR_ALIAS;
   if (rows == 0) {   // the gradient of a weight that met no row
     if (!dweight) return MXQ_OK;
-    hipLaunchKernelGGL(back_weight_kernel, dim3((uint32_t)((K + 63) / 64)), dim3(kFoldThreads), 0, stream,
-                       (const float*)nullptr, 0, (int)K, dweight);
-    return launch_status();
+    return fold_weight(nullptr, 0, K, dweight, stream);
   }
   const bool vec = K % kEPL == 0 && wide_rows(dy, ld_dy, dt) && wide_rows(x, ld_x, x_dt) && wide_rows(dresidual, ld_dresidual, x_dt) &&
                    wide_rows(dx, ld_dx, x_dt) && (!weight || aligned(weight, 16));
-  const BackArgs a{dy,  x,          weight, dresidual, ld_dy, ld_x, ld_dresidual, weight_dt == MXQ_BF16,
-                   eps, (int)rows,  (int)K, (int)back_rows_per_block(rows),       dx,   ld_dx, (float4*)workspace,
-                   dweight ? (float*)workspace + rows * 4 : nullptr};
-  if (dt == MXQ_BF16)
-    return x_dt == MXQ_BF16 ? back_launch<uint16_t, uint16_t>(a, vec, dweight, stream)
-                            : back_launch<uint16_t, uint32_t>(a, vec, dweight, stream);
-  return x_dt == MXQ_BF16 ? back_launch<uint32_t, uint16_t>(a, vec, dweight, stream)
-                          : back_launch<uint32_t, uint32_t>(a, vec, dweight, stream);
+  float2* const stats = K > kHeld ? (float2*)workspace : nullptr;
+  float* const part = (float*)workspace + (K > kHeld ? rows * 2 : 0);
+  const BackArgs a{dy,  x,         weight, dresidual, ld_dy, ld_x, ld_dresidual, weight_dt == MXQ_BF16,
+                   eps, (int)rows, (int)K, (int)back_rows_per_block(rows, K),    dx,   ld_dx, stats,
+                   dweight ? part : nullptr};
+  MXQ_TRY(dt == MXQ_BF16 ? (x_dt == MXQ_BF16 ? back_launch<uint16_t, uint16_t>(a, vec, stream)
+                                             : back_launch<uint16_t, uint32_t>(a, vec, stream))
+                         : (x_dt == MXQ_BF16 ? back_launch<uint32_t, uint16_t>(a, vec, stream)
+                                             : back_launch<uint32_t, uint32_t>(a, vec, stream)));
+  return dweight ? fold_weight(part, back_blocks(rows, K), K, dweight, stream) : MXQ_OK;
 }
 
 }  // extern "C"
