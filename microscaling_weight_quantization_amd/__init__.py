@@ -167,17 +167,21 @@ def _device_operands(fn):
     """Every tensor argument of an entry point must be a device tensor, all on one
     device: the library takes raw device pointers, and a host pointer or one
     from another GPU would reach a kernel as an invalid address."""
+    tensor = torch.Tensor
+
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         dev = -2                                            # get_device(): -1 for a host tensor
         for t in (*args, *kwargs.values()):
-            if isinstance(t, torch.Tensor):
+            if isinstance(t, tensor):
                 d = t.get_device()
+                if d == dev:
+                    continue
                 if d < 0 or not t.is_cuda:
                     raise ValueError(f"{fn.__name__}: operands must be device tensors, got one on {t.device}")
                 if dev == -2:
                     dev = d
-                elif d != dev:
+                else:
                     raise ValueError(f"{fn.__name__}: operands on cuda:{dev} and cuda:{d}; all must be on one device")
         if dev >= 0 and dev != _current_device():   # a launch goes to the current device
             with torch.cuda.device(dev):
@@ -747,10 +751,15 @@ def _library(name: str) -> ctypes.CDLL:
 
 
 def _mat(t: torch.Tensor):
-    """_matrix, at once for the usual contiguous [rows, K]."""
+    """_matrix, at once for the usual [rows, K] with contiguous rows."""
     s = t.shape
-    if len(s) == 2 and t.is_contiguous():
-        return t.data_ptr(), s[0], s[1], s[1]
+    if len(s) == 2:
+        rows, K = s
+        if t.is_contiguous():
+            return t.data_ptr(), rows, K, K
+        ld, step = t.stride()
+        if step == 1 and rows > 1:
+            return t.data_ptr(), rows, K, ld
     return _matrix(t)
 
 
@@ -802,7 +811,7 @@ def _source(x: torch.Tensor, slots: Optional[torch.Tensor], top_k: int):
 def _bytes_for(x: torch.Tensor, t: Optional[torch.Tensor], rows: int, cols: int, what: str):
     """(tensor, pointer, row stride) of a byte output, allocated if missing."""
     if t is None:
-        t = torch.empty((rows, cols), dtype=_UINT8, device=x.device)
+        t = x.new_empty((rows, cols), dtype=_UINT8)
         return t, t.data_ptr(), cols
     p, ld = _operand(t, rows, cols, what, byte=True)
     return t, p, ld
@@ -1074,11 +1083,22 @@ def _same_rows(t: torch.Tensor, rows: int, cols: int, what: str):
 def _float_out(like: torch.Tensor, out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, what: str):
     """(tensor, pointer, row stride) of a floating output shaped as `like`, allocated if missing."""
     if out is None:
-        out = torch.empty(like.shape, dtype=dtype, device=like.device)
+        out = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         return out, out.data_ptr(), cols
     if out.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {out.dtype}")
     return (out, *_same_rows(out, rows, cols, what))
+
+
+def _vector_out(like: torch.Tensor, out: Optional[torch.Tensor], shape, dtype: torch.dtype, what: str):
+    """(tensor, pointer) of a contiguous output, allocated if missing."""
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr()
+    n = 1
+    for s in shape:
+        n *= s
+    return out, _vector(out, n, dtype, what)
 
 
 def _norm_operands(x, weight, eps, residual, residual_out, y, with_y):
@@ -1145,7 +1165,7 @@ def mxq_rms_norm_fp8_group128_row_col(x: torch.Tensor, weight: Optional[torch.Te
     col_data, pcd, ldcd = _bytes_for(x, col_data, rows, K, "column payload")
     col_scale, pcs, ldcs = _bytes_for(x, col_scale, _ng(rows), K, "col_scale")
     need = L.mxq_rms_norm_fp8_group128_row_col_workspace(rows)
-    ws = torch.empty(need, dtype=_UINT8, device=x.device)
+    ws = x.new_empty((need,), dtype=_UINT8)
     _check(L, L.mxq_rms_norm_fp8_group128_row_col(*args, prd, ldrd, prs, ldrs, pcd, ldcd, pcs, ldcs, ws.data_ptr(), need,
                                                   _handle(x)))
     return row_data, row_scale, col_data, col_scale, s, y
@@ -1168,11 +1188,9 @@ def mxq_rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[to
             raise ValueError(f"dresidual must be {x.dtype}, got {dresidual.dtype}")
         pr, ldr = _same_rows(dresidual, rows, K, "dresidual")
     dx, pd, ldd = _float_out(x, dx, rows, K, x.dtype, "dx")
-    if dweight is None:
-        dweight = torch.empty(K, dtype=_FLOAT32, device=x.device)
-    pv = _vector(dweight, K, _FLOAT32, "dweight")
+    dweight, pv = _vector_out(x, dweight, (K,), _FLOAT32, "dweight")
     need = L.mxq_rms_norm_backward_workspace(rows, K)
-    ws = torch.empty(need, dtype=_UINT8, device=x.device)
+    ws = x.new_empty((need,), dtype=_UINT8)
     _check(L, L.mxq_rms_norm_backward(pg, ldg, _float_code(dy), px, ldx, _float_code(x), pw, wdt, eps, pr, ldr, rows, K,
                                       pd, ldd, pv, ws.data_ptr(), need, _handle(x)))
     return dx, dweight
@@ -1288,11 +1306,8 @@ def mxq_route_experts(logits: torch.Tensor, top_k: int, bias: Optional[torch.Ten
         pm = mask.data_ptr()
     if top_k < 1:
         raise ValueError(f"top_k is at least 1, got {top_k}")
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=_INT32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=_FLOAT32, device=logits.device)
-    pi, pw = _vector(ids, T * top_k, _INT32, "ids"), _vector(weights, T * top_k, _FLOAT32, "weights")
+    ids, pi = _vector_out(logits, ids, (T, top_k), _INT32, "ids")
+    weights, pw = _vector_out(logits, weights, (T, top_k), _FLOAT32, "weights")
     _check(L, L.mxq_route_experts(pl, ldl, T, E, _float_code(logits), pb, pm, _named(_SCORES, score, "score"), renormalize,
                                   scale, n_groups, top_groups, group_top, top_k, pi, pw, _handle(logits)))
     return ids, weights
