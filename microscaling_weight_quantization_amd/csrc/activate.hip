@@ -75,9 +75,9 @@ struct Raw {
   Chunk<T> gate, up, da;
 };
 // kOnce: each line is read by one instruction and by no other workgroup, and leaves with the non-temporal hint.  That holds
-// for bf16 (a lane's 32 bytes of fp32 are two loads, each of half of every line): 49152 x 1024 bf16 forward 55.9 -> 54.1 us,
-// backward 106.3 -> 94.2; 16000 x 1024 fp32 29.9 -> 34.2 and 51.6 -> 55.6, so not there; and 16000 x 1000 bf16 backward,
-// where two workgroups read each line, 53.5 -> 60.5.
+// for bf16 (a lane's 32 bytes of fp32 are two loads, each of half of every line): 49152 x 1024 bf16 both ways 61.8 -> 53.9
+// us, 2048 x 28672 by rows 51.0 -> 46.5; 16000 x 1024 fp32 29.9 -> 34.2, so not there, nor for 16000 x 1000 bf16 backward,
+// where two workgroups read each line (53.5 -> 60.5).
 template <typename T, bool kVec, bool kOnce, bool kBack>
 __device__ __forceinline__ void load_raw(Raw<T, kBack>& v, const ActArgs& s, int64_t r, int c) {
   v.gate = load_chunk<T, kVec, kOnce>((const T*)s.gate + r * s.ld_gate, c, s.F);
@@ -136,13 +136,13 @@ __global__ __launch_bounds__(kRowThreads) void act_rows_kernel(ActArgs s, MxqDiv
   const uint32_t r = mxq_quot(g, groups), b = g - r * groups.d;
   const int c = (int)b * kGroup + (threadIdx.x & 15) * kEPL;
   Raw<T, false> v;
-  load_raw<T, kVec, false>(v, s, r, c);
+  load_raw<T, kVec, kVec && sizeof(T) == 2>(v, s, r, c);
   store_group<kVec, false>(data + (int64_t)r * ld_data, scale + (int64_t)r * scale_ld, c, s.F,
                            value_of<T, kAct>(v, s.up != nullptr));
 }
 
 // ---- groups along both -----------------------------------------------------------------
-template <typename T, int kAct, bool kVec, bool kWhole, int kRows>
+template <typename T, int kAct, bool kVec, bool kStream, bool kWhole, int kRows>
 __device__ __forceinline__ void act_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
                                          TileShared<kRows>& shared) {
   Chunk<uint32_t> v[kRows];
@@ -156,10 +156,10 @@ __device__ __forceinline__ void act_tile(const ActArgs& s, const TileRows& t, in
 #pragma unroll
     for (int i = 0; i < kAtOnce; i++) v[i0 + i] = narrow<uint32_t>(value_of<T, kAct>(raw[i], s.up != nullptr));
   }
-  store_tile<uint32_t, kVec, true, false, kWhole>(v, out, t, id, blockIdx.x, shared);
+  store_tile<uint32_t, kVec, true, kStream, kWhole>(v, out, t, id, blockIdx.x, shared);
 }
 
-template <typename T, int kAct, bool kVec, int kRows>
+template <typename T, int kAct, bool kVec, bool kStream, int kRows>
 __global__ __launch_bounds__(16 * kGroup / kRows) void act_tiles_kernel(ActArgs s, int first_id, int rows,
                                                                         const int32_t* offsets, int experts,
                                                                         TileOut out) {
@@ -169,8 +169,8 @@ __global__ __launch_bounds__(16 * kGroup / kRows) void act_tiles_kernel(ActArgs 
   const TileRows t = tile_rows(offsets, experts, rows, id, shared);
   if (!t.owned) clear_codes(out, id, blockIdx.x);
   if (t.first >= t.hi) return;   // the same for the whole workgroup
-  if (kVec && whole_tile(t, blockIdx.x, s.F)) act_tile<T, kAct, kVec, kVec, kRows>(s, t, id, out, shared);
-  else act_tile<T, kAct, kVec, false, kRows>(s, t, id, out, shared);
+  if (kVec && whole_tile(t, blockIdx.x, s.F)) act_tile<T, kAct, kVec, kStream, kVec, kRows>(s, t, id, out, shared);
+  else act_tile<T, kAct, kVec, kStream, false, kRows>(s, t, id, out, shared);
 }
 
 // ---- backward ----------------------------------------------------------------------------
@@ -219,7 +219,7 @@ __device__ __forceinline__ f32x8 gradient_at(const ActArgs& s, int64_t r, int c)
 // lie in one of the halves or across their border.
 enum Part { kBothHalves, kGateHalf, kUpHalf, kBorder };
 
-template <typename T, int kAct, bool kVec, Part kPart, bool kWhole, int kRows>
+template <typename T, int kAct, bool kVec, bool kStream, Part kPart, bool kWhole, int kRows>
 __device__ __forceinline__ void act_backward_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
                                                   TileShared<kRows>& shared) {
   constexpr int kStep = kGroup / kRows;
@@ -250,12 +250,12 @@ __device__ __forceinline__ void act_backward_tile(const ActArgs& s, const TileRo
         if (i == j) v[j] = one;
     }
   }
-  store_tile<uint32_t, kVec, true, false, kWhole>(v, out, t, id, blockIdx.x, shared);
+  store_tile<uint32_t, kVec, true, kStream, kWhole>(v, out, t, id, blockIdx.x, shared);
   if constexpr (kPart == kBothHalves)
-    store_tile<uint32_t, kVec, true, false, kWhole, true>(u, out, t, id, blockIdx.x + s.F / kGroup, shared);
+    store_tile<uint32_t, kVec, true, kStream, kWhole, true>(u, out, t, id, blockIdx.x + s.F / kGroup, shared);
 }
 
-template <typename T, int kAct, bool kVec, bool kBoth, int kRows>
+template <typename T, int kAct, bool kVec, bool kStream, bool kBoth, int kRows>
 __global__ __launch_bounds__(16 * kGroup / kRows) void act_backward_kernel(ActArgs s, int first_id, int rows,
                                                                            const int32_t* offsets, int experts,
                                                                            TileOut out) {
@@ -270,16 +270,16 @@ __global__ __launch_bounds__(16 * kGroup / kRows) void act_backward_kernel(ActAr
   if (t.first >= t.hi) return;   // all of this is the same for the whole workgroup
   const bool whole = kVec && whole_tile(t, blockIdx.x, kBoth ? s.F : out.K);
   if constexpr (kBoth) {
-    if (whole) act_backward_tile<T, kAct, kVec, kBothHalves, kVec, kRows>(s, t, id, out, shared);
-    else act_backward_tile<T, kAct, kVec, kBothHalves, false, kRows>(s, t, id, out, shared);
+    if (whole) act_backward_tile<T, kAct, kVec, kStream, kBothHalves, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kStream, kBothHalves, false, kRows>(s, t, id, out, shared);
   } else if (c + kGroup <= s.F || !s.up) {
-    if (whole) act_backward_tile<T, kAct, kVec, kGateHalf, kVec, kRows>(s, t, id, out, shared);
-    else act_backward_tile<T, kAct, kVec, kGateHalf, false, kRows>(s, t, id, out, shared);
+    if (whole) act_backward_tile<T, kAct, kVec, kStream, kGateHalf, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kStream, kGateHalf, false, kRows>(s, t, id, out, shared);
   } else if (c >= s.F) {
-    if (whole) act_backward_tile<T, kAct, kVec, kUpHalf, kVec, kRows>(s, t, id, out, shared);
-    else act_backward_tile<T, kAct, kVec, kUpHalf, false, kRows>(s, t, id, out, shared);
+    if (whole) act_backward_tile<T, kAct, kVec, kStream, kUpHalf, kVec, kRows>(s, t, id, out, shared);
+    else act_backward_tile<T, kAct, kVec, kStream, kUpHalf, false, kRows>(s, t, id, out, shared);
   } else {
-    act_backward_tile<T, kAct, kVec, kBorder, false, kRows>(s, t, id, out, shared);
+    act_backward_tile<T, kAct, kVec, kStream, kBorder, false, kRows>(s, t, id, out, shared);
   }
 }
 
@@ -334,7 +334,7 @@ int launch_rows(const ActArgs& a, int64_t rows, bool vec, uint8_t* data, int64_t
 }
 
 // Rows a lane: four, in workgroups of 512, forward; eight, in workgroups of 256, backward, where four take 131 registers
-// and so leave one workgroup a CU.  49152 x 1024 forward 53.9 us (eight: 54.6), backward 92.8 (four: 112.9).
+// and so leave one workgroup a CU.  49152 x 1024 forward 53.9 us (eight: 54.6), backward 98.1 (four: 119).
 constexpr int kForwardRows = 4, kBackwardRows = 8;
 
 template <typename T, int kAct>
@@ -343,6 +343,9 @@ int launch_tiles(const ActArgs& a, int64_t rows, bool vec, const int32_t* offset
   const int64_t tiles = out.code_rows + (offsets ? 2 : 0);   // the rows of no expert, behind and before the others, may take two more
   constexpr int64_t kStep = 65535;   // of a grid's second dimension
   const bool both = a.da && a.up && a.F % kGroup == 0;
+  // Payloads that fill half of the last-level cache leave with the non-temporal hint: forward 8192 x 14336 130.8 -> 125.4 us,
+  // 49152 x 1024 53.9 -> 56.3; backward 49152 x 1024 103.6 -> 98.1.
+  const bool big = rows * out.K > (int64_t)64 << 20;
   const int64_t columns = both ? a.F / kGroup : groups_of(out.K);
 #define MXQ_ACT_LAUNCH(kRows, ...)                                                                                     \
   hipLaunchKernelGGL((__VA_ARGS__, kRows>), grid, dim3(16 * kGroup / kRows), 0, stream, a, (int)t, (int)rows, offsets, \
@@ -350,14 +353,16 @@ int launch_tiles(const ActArgs& a, int64_t rows, bool vec, const int32_t* offset
   for (int64_t t = 0; t < tiles; t += kStep) {
     const dim3 grid((uint32_t)columns, (uint32_t)std::min(kStep, tiles - t));
     if (!a.da) {
-      if (vec) MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, true);
-      else MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, false);
+      if (!vec) MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, false, false);
+      else if (big) MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, true, true);
+      else MXQ_ACT_LAUNCH(kForwardRows, act_tiles_kernel<T, kAct, true, false);
     } else if (both) {
-      if (vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, true);
-      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, true);
+      if (!vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, false, true);
+      else if (big) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, true, true);
+      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, false, true);
     } else {
-      if (vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, false);
-      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, false);
+      if (vec) MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, true, false, false);
+      else MXQ_ACT_LAUNCH(kBackwardRows, act_backward_kernel<T, kAct, false, false, false);
     }
     const int st = launch_status();
     if (st != MXQ_OK) return st;

@@ -441,6 +441,7 @@ int norm_rows(const NormArgs& a, hipStream_t stream) {
   if (K <= 128 * 8) return launch_norm<TX, TS, 128, 1, kVec, kStream>(a, stream);
   if (K <= 256 * 8) return launch_norm<TX, TS, 256, 1, kVec, kStream>(a, stream);
   if (K <= 512 * 8) return launch_norm<TX, TS, 512, 1, kVec, kStream>(a, stream);
+  if (K <= 640 * 8) return launch_norm<TX, TS, 640, 1, kVec, kStream>(a, stream);
   if (K <= 768 * 8) return launch_norm<TX, TS, 768, 1, kVec, kStream>(a, stream);
   if (K <= 1024 * 8) return launch_norm<TX, TS, 1024, 1, kVec, kStream>(a, stream);
   if (K <= 1024 * 16) return launch_norm<TX, TS, 1024, 2, kVec, kStream>(a, stream);
@@ -536,13 +537,13 @@ int norm_entry(const void* x, int64_t ld_x, const void* residual, int64_t ld_res
 constexpr int kHeld = 1024 * 16;   // elements of a row that registers hold
 // Lanes of a workgroup of the backward pass.
 int back_threads(int64_t K) {
-  for (int lanes : {64, 128, 256, 512, 768})
+  for (int lanes : {64, 128, 256, 512, 640, 768})
     if (K <= lanes * 8) return lanes > 64 ? lanes : kThreads;
   return 1024;
 }
 // Rows of a workgroup: as many workgroups as have 1024 lanes for each CU (8192 x 8192 bf16 108.5 us; twice as many 115).
 int64_t back_rows_per_block(int64_t rows, int64_t K) {
-  const int64_t fill = K > kHeld ? 256 : 256 * 1024 / back_threads(K);
+  const int64_t fill = K > kHeld ? 256 : 256 * (1024 / back_threads(K));
   return std::max<int64_t>(K > kHeld ? 4 : 1, (rows + fill - 1) / fill);
 }
 int64_t back_blocks(int64_t rows, int64_t K) {
@@ -565,6 +566,7 @@ int back_rows(const BackArgs& a, hipStream_t stream) {
   if (K <= 128 * 8) return launch_back<TY, TS, 128, 1, kVec>(a, stream);
   if (K <= 256 * 8) return launch_back<TY, TS, 256, 1, kVec>(a, stream);
   if (K <= 512 * 8) return launch_back<TY, TS, 512, 1, kVec>(a, stream);
+  if (K <= 640 * 8) return launch_back<TY, TS, 640, 1, kVec>(a, stream);
   if (K <= 768 * 8) return launch_back<TY, TS, 768, 1, kVec>(a, stream);
   if (K <= 1024 * 8) return launch_back<TY, TS, 1024, 1, kVec>(a, stream);
   if (K <= kHeld) return launch_back<TY, TS, 1024, 2, kVec>(a, stream);

@@ -53,7 +53,7 @@ def check_norm(rows, K, dtype, stream, with_res, w_dtype, place, seed, cols):
 
 
 # every number of lanes and pieces that a row takes, and its borders
-WIDTHS = [1, 7, 8, 127, 128, 129, 512, 520, 1000, 2048, 2049, 2056, 4096, 4104, 8191, 8192, 8200, 16384, 16385, 16400, 20000]
+WIDTHS = [1, 7, 8, 127, 128, 129, 512, 520, 1000, 2048, 2049, 2056, 4096, 4104, 5120, 5128, 6000, 6144, 6152, 8191, 8192, 8200, 16384, 16385, 16400, 20000]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
