@@ -41,12 +41,12 @@ __device__ __forceinline__ f32x8 weight_at(const void* w, bool bf16, int c, int 
   return bf16 ? load_floats<uint16_t, kVec>(w, c, K) : load_floats<uint32_t, kVec>(w, c, K);
 }
 
-// Elements [c, c + 8) of s of a row.
-template <typename TX, typename TS, bool kVec>
+// Elements [c, c + 8) of s of a row.  kOnce: loads carry the non-temporal hint.
+template <typename TX, typename TS, bool kVec, bool kOnce = false>
 __device__ __forceinline__ f32x8 stream_at(const NormArgs& a, int64_t row, int c) {
-  const f32x8 x = load_floats<TX, kVec>((const TX*)a.x + row * a.ld_x, c, a.K);
+  const f32x8 x = load_floats<TX, kVec, kOnce>((const TX*)a.x + row * a.ld_x, c, a.K);
   if (!a.residual) return x;
-  const f32x8 r = load_floats<TS, kVec>((const TS*)a.residual + row * a.ld_res, c, a.K);
+  const f32x8 r = load_floats<TS, kVec, kOnce>((const TS*)a.residual + row * a.ld_res, c, a.K);
   return widen<TS>(narrow<TS>(x + r));
 }
 
@@ -84,7 +84,7 @@ template <int kLanes>
 constexpr int kNormThreads = kLanes > 64 ? kLanes : kThreads;
 
 // A row in the registers of kLanes lanes, kChunks pieces of eight elements each.  kStream: outputs leave with the
-// non-temporal hint.
+// non-temporal hint; otherwise the inputs come with it, so that the caches keep the sum for the columns.
 template <typename TX, typename TS, int kLanes, int kChunks, bool kVec, bool kStream>
 __global__ __launch_bounds__(kNormThreads<kLanes>) void norm_kernel(NormArgs a) {
   keep_denormals();
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kNormThreads<kLanes>) void norm_kernel(NormArgs a) 
 #pragma unroll
   for (int i = 0; i < kChunks; i++) {
     const int c = (i * kLanes + lane) * kEPL;
-    s[i] = stream_at<TX, TS, kVec>(a, row, c);
+    s[i] = stream_at<TX, TS, kVec, kVec && !kStream>(a, row, c);
   }
 #pragma unroll
   for (int i = 0; i < kChunks; i++) sum = add_squares(s[i], sum);
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kTileThreads) void norm_columns_kernel(NormArgs a, 
     f32x8 s{};
     float root = 0;
     if (r < a.rows) {
-      s = a.sum ? load_floats<TS, kVec>((const TS*)a.sum + r * a.ld_sum, c, a.K) : stream_at<TX, TS, kVec>(a, r, c);
+      s = a.sum ? load_floats<TS, kVec, kVec && sizeof(TS) == 2>((const TS*)a.sum + r * a.ld_sum, c, a.K) : stream_at<TX, TS, kVec>(a, r, c);
       root = a.stats[r];
     }
     v[i] = narrow<uint32_t>(s * root * w);
@@ -473,7 +473,8 @@ int norm_columns(const NormArgs& a, const TileOut& out, bool vec, hipStream_t st
 template <typename TX, typename TS>
 int norm_launch(const NormArgs& a, const TileOut* columns, bool vec, hipStream_t stream) {
   // The hint for outputs that nothing reads at once: not for a sum that the columns come from.  8192 x 8192 bf16 106 ->
-  // 102 us, 2048 x 8192 27.4 -> 22.9; rows and columns of 4096 x 8192 with the hint 92.8 -> 99.0.
+  // 102 us, 2048 x 8192 27.4 -> 22.9; rows and columns of 4096 x 8192 with the hint 92.8 -> 99.0.  There the inputs have it:
+  // 99.3 -> 95.9, 8192 x 8192 bf16 122.9 -> 114.2.
   MXQ_TRY(!vec      ? (norm_rows<TX, TS, false, false>(a, stream))
           : columns ? (norm_rows<TX, TS, true, false>(a, stream))
                     : (norm_rows<TX, TS, true, true>(a, stream)));
