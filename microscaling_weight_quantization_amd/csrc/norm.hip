@@ -190,7 +190,7 @@ struct BackArgs {
   int64_t ld_dy, ld_s, ld_dres;
   bool w_bf16;
   float eps;
-  int rows, K, per_block;   // rows of a workgroup (of a block, where rows are long)
+  int rows, K, per_block;   // rows of a block, where rows are long
   void* dx;
   int64_t ld_dx;
   float2* stats;            // r and mean(g u) of each row, where rows are long
@@ -204,9 +204,10 @@ struct BackRow {
   Chunk<TY> dy[kChunks];
 };
 
-// A workgroup takes per_block rows one after the other (as many at a time as it has lanes for), the next row on its way while
-// this one is worked out, and keeps its part of dw in registers.  Loads with the non-temporal hint, stores without: 8192 x 8192
-// bf16 99.9 us, plain loads 113, stores with it as well 102.5, loads without and stores with it 109.
+// A workgroup takes a row (as many as it has lanes for), and then every one as many rows further as the card works on at
+// once, the next row on its way while this one is worked out; it keeps its part of dw in registers.  8192 x 8192 bf16 96.5
+// us; 102.0 where each takes a run of neighbouring rows.  Loads with the non-temporal hint, stores without: so 99.9, plain
+// loads 113, stores with it as well 102.5, loads without and stores with it 109, all in such runs.
 template <typename TY, typename TS, int kLanes, int kChunks, bool kVec>
 __global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) {
   keep_denormals();
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) 
   __shared__ float2 meet[2][16];
   __shared__ float fold[kSlots > 1 ? kSlots : 1][kSlots > 1 ? kLanes * kEPL : 1];
   const int slot = kSlots > 1 ? threadIdx.x / kLanes : 0, lane = threadIdx.x % kLanes;
-  const int64_t lo = (int64_t)blockIdx.x * a.per_block, hi = min(lo + a.per_block, (int64_t)a.rows);
+  const int64_t lo = (int64_t)blockIdx.x * kSlots, hi = a.rows, step = (int64_t)gridDim.x * kSlots;
   f32x8 w[kChunks], dw[kChunks];
 #pragma unroll
   for (int i = 0; i < kChunks; i++) {
@@ -283,19 +284,19 @@ __global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) 
   };
   Row even;
   if constexpr (kChunks > 1) {   // two rows of these would not fit into the registers
-    for (int64_t row = lo + slot; row - slot < hi; row += kSlots) {
+    for (int64_t row = lo + slot; row - slot < hi; row += step) {
       load(even, row);
       work(even, row);
     }
   } else {
     Row odd;
     load(even, lo + slot);
-    for (int64_t row = lo + slot; row - slot < hi; row += 2 * kSlots) {
-      load(odd, row + kSlots);
+    for (int64_t row = lo + slot; row - slot < hi; row += 2 * step) {
+      load(odd, row + step);
       work(even, row);
-      if (row - slot + kSlots >= hi) break;
-      load(even, row + 2 * kSlots);
-      work(odd, row + kSlots);
+      if (row - slot + step >= hi) break;
+      load(even, row + 2 * step);
+      work(odd, row + step);
     }
   }
   if (!a.part) return;   // the same for all

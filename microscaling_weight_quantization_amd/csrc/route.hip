@@ -341,13 +341,15 @@ __device__ __forceinline__ void sort_falling(double* v) {
           if (j + i + k < n && (j + i) / (2 * p) == (j + i + k) / (2 * p)) order(v[j + i], v[j + i + k]);
 }
 
-constexpr double kOpen = -0x1p995, kShut = -0x1p1000, kHuge = 0x1p990;   // open keys lie above kOpen
+constexpr double kOpen = -0x1p995, kShut = -0x1p1000;   // open keys lie above kOpen
 
+// kExact: the key's lowest nine bits are 0, as those of an fp32 value.  An infinite key above makes a NaN, whose token is in
+// doubt anyway.
+template <bool kExact>
 __device__ __forceinline__ double with_index(double key, int e) {
-  // infinities become numbers
-  const double v = fmin(fmax(key, kShut), kHuge);
-  u32x2 b = __builtin_bit_cast(u32x2, v);
-  b[0] = (b[0] & ~(uint32_t)(kMost - 1)) | (uint32_t)(e ^ (v < 0 ? 0 : kMost - 1));
+  u32x2 b = __builtin_bit_cast(u32x2, max64(key, kShut));
+  const uint32_t at = (uint32_t)(kMost - 1 - e) ^ ((uint32_t)((int)b[1] >> 31) & (kMost - 1));   // e itself below 0
+  b[0] = (kExact ? b[0] : b[0] & ~(uint32_t)(kMost - 1)) | at;
   return __builtin_bit_cast(double, b);
 }
 __device__ __forceinline__ int index_of(double v) {
@@ -485,7 +487,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m,
   double d[kEach], v[kList];
 #pragma unroll
   for (int i = 0; i < kEach; i++)   // + 0: of the zeros one is as good as the other
-    d[i] = with_index(kept ? (double)(key[i] + 0) : -S::kInfinite, min(m.base + i, kMost - 1));
+    d[i] = with_index<sizeof(F) == 4>(kept ? (double)(key[i] + 0) : -S::kInfinite, min(m.base + i, kMost - 1));
   largest_of<kEach, kList>(d, v);
   merge_lanes<kXor1>(v);
   merge_lanes<kXor2>(v);

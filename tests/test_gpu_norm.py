@@ -157,6 +157,28 @@ def test_norm_backward_types(rows, K, dtype, x_dtype):
     check_backward(rows, K, dtype, x_dtype, None, False, lambda t: t.to(DEV), rows + K + 1)
 
 
+@pytest.mark.parametrize("K", [96, 400, 3000, 20000])
+def test_norm_backward_extremes(K):
+    """Squares that overflow in some rows and not in their neighbours; a row of an Inf or NaN spoils dx of its own alone."""
+    g = gen(K)
+    x, dy = torch.randn(9, K, generator=g), torch.randn(9, K, generator=g)
+    x[0] *= 1e30
+    x[3] = 3.3e38
+    x[4] *= 1e25
+    x[6] *= 1e-30
+    for dtype in (FP32, BF16):
+        v, d = x.to(dtype), dy.to(dtype)
+        (dx, dx_off), (dw, dw_off) = ref.norm_backward(d, ref.f64(v), None, EPS, None)
+        got, got_w = mxq.mxq_rms_norm_backward(d.to(DEV), v.to(DEV), None, EPS)
+        # r of the second row is below 2^-126 and has 20 places or more
+        ref.check_values(got, dx, dx_off + dx.abs() * 2.0 ** -20 + 2.0 ** -147, "dx")
+        ref.check_values(got_w, dw, dw_off + dy.abs().sum(0).double() * 2.0 ** -20, "dweight")
+        v[4, 5], v[8, K - 1] = float("inf"), float("nan")
+        spoilt, _ = mxq.mxq_rms_norm_backward(d.to(DEV), v.to(DEV), None, EPS)
+        keep = [r for r in range(9) if r not in (4, 8)]
+        assert torch.equal(spoilt[keep], got[keep]) and bool(torch.isnan(spoilt[8]).all())
+
+
 def test_norm_backward_against_differences():
     """dx and dweight against differences of the forward call itself: f = <y, dy> moved by a step along a direction.  With
     fp32 values of about 1 a difference of two sums of n = 80 products is off by 2 n 2^-24 |terms| / (2 h), h = 2^-6, and by
@@ -194,6 +216,27 @@ def test_norm_leading_dimensions_and_empty():
     assert torch.equal(y.view(15, 200), flat)
     q, c, _, _ = mxq.mxq_rms_norm_fp8_group128(x[:0], None, EPS)
     assert q.shape == (0, 200) and c.shape == (0, 2)
+
+
+def test_norm_operands_at_any_address():
+    """Weights, rows and gradients that begin at odd elements; rows that all lie in one place are refused."""
+    g = gen(9)
+    buf = torch.randn(4000, generator=g)
+    w = buf[3:3 + 264]
+    x = values(40, 264, g, BF16)
+    want, off = ref.norm(ref.f64(x), w, EPS)
+    wd, xd = buf.to(DEV)[3:3 + 264], odd_view(x, 1, 3)
+    y, _ = mxq.mxq_rms_norm(xd, wd, EPS)
+    ref.check_values(y, want, off, "y")
+    dy = values(40, 264, g, FP32, 2)
+    (dx, dx_off), (dw, dw_off) = ref.norm_backward(dy, ref.f64(x), w, EPS, None)
+    got, got_w = mxq.mxq_rms_norm_backward(odd_view(dy, 1, 1), xd, wd, EPS)
+    ref.check_values(got, dx, dx_off, "dx")
+    ref.check_values(got_w, dw, dw_off, "dweight")
+    with pytest.raises(mxq.MxqError):
+        mxq.mxq_rms_norm(x[:1].to(DEV).expand(5, 264), None, EPS)
+    with pytest.raises(mxq.MxqError):
+        mxq.mxq_rms_norm(x.to(DEV), None, 0.0)
 
 
 def test_norm_leaves_the_rest_alone():

@@ -145,6 +145,25 @@ def test_route_values_that_are_not_finite():
             assert torch.equal(got[keep], w[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_route_masks_of_the_lowest_value(dtype):
+    """Logits of the type's lowest value are open and last; a token that has no others shares its weight out evenly."""
+    l = logits_of(30, 96, 19, dtype)
+    low = torch.finfo(dtype).min
+    l[:, 10:80] = low
+    l[4] = low
+    l[5, 3:] = low
+    for score in ("softmax", "sigmoid"):
+        for how in ({}, {"n_groups": 8, "top_groups": 8}, {"n_groups": 8, "top_groups": 2}):
+            want, _ = ref.route(l, 5, score=score, **how)
+            ids, w = mxq.mxq_route_experts(l.to(DEV), 5, score=score, **how)
+            assert torch.equal(ref.host(ids), want)
+            assert bool(torch.isfinite(w).all()) and torch.allclose(w.sum(1).cpu(), torch.ones(30), atol=1e-6)
+            assert torch.allclose(w[4].cpu(), torch.full((5,), 0.2))
+            d = mxq.mxq_route_experts_backward(w, l.to(DEV), ids, score=score)
+            assert bool(torch.isfinite(d).all())
+
+
 def test_route_backward_of_ids_out_of_range_and_named_twice():
     """Ids that are no expert's count nothing; an expert named twice gets the sum."""
     l = logits_of(6, 20, 12)
