@@ -620,7 +620,7 @@ int mxq_combine_rows_backward(const void* dy, int64_t ld_dy, const void* rows, i
  *   x         [rows, K] of type dt, row stride ld_x >= K
  *   residual  [rows, K] of type residual_dt; NULL: none, and residual_dt is not looked at
  *   weight    [K] of type weight_dt, contiguous; NULL: all 1
- *   eps       positive and finite (MXQ_ERR_SHAPE otherwise)
+ *   eps       finite and at least 2^-126 (MXQ_ERR_SHAPE otherwise)
  *   sum       [rows, K] of type residual_dt: s.  NULL: not wanted; MXQ_ERR_NULL where it is
  *             wanted without a residual.  sum == residual with the same row stride (in place) is
  *             allowed.

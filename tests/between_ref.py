@@ -2,7 +2,7 @@
 activation, the routing -- on the CPU, for the tests, and how far a kernel may be from them.
 
 A rounding to a type is off by at most half a step, eps / 2 of the value: HALF for
-fp32, 2^-9 for bf16, 2^-4 of the value or 2^-10 of the scale for E4M3.  Kernels work in
+fp32, 2^-8 for bf16, 2^-4 of the value or 2^-10 of the scale for E4M3.  Kernels work in
 fp32; `rel` below counts the steps 2 HALF of what is computed.
 """
 from __future__ import annotations

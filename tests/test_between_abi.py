@@ -77,6 +77,16 @@ def test_norm_refusals(lib, which):
         assert lib.mxq_rms_norm_fp8_group128_row_col_workspace(-1) == 0
 
 
+@pytest.mark.parametrize("which", [0, 1, 2, 3])
+def test_norm_least_eps(lib, which):
+    """Squares below 2^-149 vanish, which an eps of a normal number hides; a smaller one is refused."""
+    d = dict(dy=0x100000, ld_dy=300, dt=0, x=0x200000, ld_x=300, x_dt=1, w=0x300000, w_dt=1, eps=1e-6, dres=None, ld_dres=300,
+             rows=0, K=300, dx=0x500000, ld_dx=300, dw=None, ws=None, bytes=0, stream=None)
+    fn, d = (norm_calls(lib) + [(lib.mxq_rms_norm_backward, d)])[which]
+    assert call(fn, d, rows=0, eps=2.0 ** -126) == OK
+    assert call(fn, d, rows=0, eps=2.0 ** -126 - 2.0 ** -149) == SHAPE and call(fn, d, rows=0, eps=1e-40) == SHAPE
+
+
 def test_norm_backward_refusals(lib):
     fn = lib.mxq_rms_norm_backward
     need = lib.mxq_rms_norm_backward_workspace(200, 300)

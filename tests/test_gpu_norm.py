@@ -179,6 +179,24 @@ def test_norm_backward_extremes(K):
         assert torch.equal(spoilt[keep], got[keep]) and bool(torch.isnan(spoilt[8]).all())
 
 
+@pytest.mark.parametrize("K", [96, 400, 3000, 20000])
+def test_norm_backward_of_large_gradients(K):
+    """Rows whose sum of g s passes 2^128, with and without the sum of squares, where dx does not."""
+    g = gen(K + 1)
+    x, dy = torch.randn(5, K, generator=g), torch.randn(5, K, generator=g)
+    x[0] *= 1e4
+    x[2] *= 1e30
+    dy[0] *= 1e36
+    dy[2] *= 1e36
+    dy[3] *= 1e36
+    for dtype in (FP32, BF16):
+        v, d = x.to(dtype), dy.to(dtype)
+        (dx, dx_off), (dw, dw_off) = ref.norm_backward(d, ref.f64(v), None, EPS, None)
+        got, got_w = mxq.mxq_rms_norm_backward(d.to(DEV), v.to(DEV), None, EPS)
+        ref.check_values(got, dx, dx_off + 2.0 ** -147, "dx")
+        ref.check_values(got_w, dw, dw_off, "dweight")
+
+
 def test_norm_backward_against_differences():
     """dx and dweight against differences of the forward call itself: f = <y, dy> moved by a step along a direction.  With
     fp32 values of about 1 a difference of two sums of n = 80 products is off by 2 n 2^-24 |terms| / (2 h), h = 2^-6, and by
