@@ -7,6 +7,10 @@
 //   dgate = da up act'(gate), dup = da act(gate)
 //
 // Everything is computed in fp32 and rounded once, to E4M3.
+//
+// Memory bounds it; every element is read once.  2048 x 28672 bf16 by rows 47.2 us (294 MB, 6.2 TB/s, a plain copy's rate
+// being 6.6); both ways 128 rows x 128 columns a workgroup, of whose rows it touches 256 bytes each: 49152 x 1024 53.6 us
+// (303 MB, 5.6 TB/s), its gradients 97 (505 MB, 5.2), which two workgroups a CU hold in 170 registers a lane.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -334,7 +338,7 @@ int launch_rows(const ActArgs& a, int64_t rows, bool vec, uint8_t* data, int64_t
 }
 
 // Rows a lane: four, in workgroups of 512, forward; eight, in workgroups of 256, backward, where four take 131 registers
-// and so leave one workgroup a CU.  49152 x 1024 forward 53.9 us (eight: 54.6), backward 98.1 (four: 119).
+// and so leave one workgroup a CU.  49152 x 1024 forward 53.6 us (eight: 54.6), backward 97 (four: 119).
 constexpr int kForwardRows = 4, kBackwardRows = 8;
 
 template <typename T, int kAct>

@@ -10,9 +10,14 @@
 //              sigmoid:  dl_e = p_e (1 - p_e) h_e
 //              where the weights sum to scale, p_j h_j = w_j (g_j - sum g w / scale), for both,
 //              and sum h p = 0
+//
+// Instructions bound the choice, about 1200 a wave of four tokens, most of them comparisons in pairs: 16384 fp32 tokens of 256
+// experts with a bias and 8 groups 14.0 us, 131072 of them 63.6 (2.2 TB/s); 131072 bf16 tokens of 128 experts 27.5.
+// Gradients of 131072 bf16 tokens of 128 experts take 23.9 us, 6.0 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "checks.h"
 #include "fastdiv.h"
@@ -100,169 +105,184 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The largest of the wave's keys, the lowest index where several are equal; element lane + 64 i is key[i].
-struct Best {
-  double key;
-  int at;
-};
-__device__ __forceinline__ Best better(Best a, Best b) {
-  return b.key > a.key || (b.key == a.key && b.at < a.at) ? b : a;
-}
-template <int CTRL>
-__device__ __forceinline__ Best better_row(Best b) {
-  return better(b, Best{row_dpp<CTRL>(b.key), (int)dpp<CTRL>((uint32_t)b.at)});
-}
-__device__ __forceinline__ Best best_of(const double (&key)[kPer], int count) {
-  const int lane = threadIdx.x & 63;
-  Best b{key[0], lane};
-#pragma unroll
-  for (int i = 1; i < kPer; i++)
-    if (64 * i < count && key[i] > b.key) b = Best{key[i], lane + 64 * i};
-  b = better_row<kXor1>(b);
-  b = better_row<kXor2>(b);
-  b = better_row<kXor4>(b);
-  b = better_row<kXor8>(b);
-  Two k = rows_of_two(b.key);
-  u32x2 at = swap16((uint32_t)b.at, (uint32_t)b.at);
-  b = better(Best{k.a, (int)at[0]}, Best{k.b, (int)at[1]});
-  k = halves_of(b.key);
-  at = swap32((uint32_t)b.at, (uint32_t)b.at);
-  return better(Best{k.a, (int)at[0]}, Best{k.b, (int)at[1]});
-}
-__device__ __forceinline__ void take(double (&key)[kPer], int at) {
-#pragma unroll
-  for (int i = 0; i < kPer; i++)
-    if (at == (int)(threadIdx.x & 63) + 64 * i) key[i] = kClosed;
+// The larger and the smaller of two numbers (neither of these is a NaN, so nothing needs to be made quiet first).
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
 }
 
-// What a wave needs in LDS: keys and values of the experts, the chosen ones, the groups that are kept.
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// What a wave needs in LDS: the experts' values and logits, the groups' values and which of them are kept, the choice.
 struct WaveLds {
-  double *key, *value;
+  double *value, *rank;
+  float* logit;
   int32_t* chosen;
   uint8_t* kept;
   __host__ __device__ static size_t bytes(int experts, int top_k, int groups) {
-    return ((size_t)experts * 16 + (size_t)top_k * 4 + groups + 15) / 16 * 16;
+    return ((size_t)experts * 12 + (size_t)top_k * 4 + (size_t)groups * 9 + 15) / 16 * 16;
   }
   __device__ __forceinline__ WaveLds(char* lds, const RouteArgs& a) {
-    key = (double*)(lds + threadIdx.x / 64 * bytes(a.experts, a.top_k, a.groups));
-    value = key + a.experts;
-    chosen = (int32_t*)(value + a.experts);
+    value = (double*)(lds + threadIdx.x / 64 * bytes(a.experts, a.top_k, a.groups));
+    rank = value + a.experts;
+    logit = (float*)(rank + a.groups);
+    chosen = (int32_t*)(logit + a.experts);
     kept = (uint8_t*)(chosen + a.top_k);
   }
 };
 
-template <bool kBf16>
+// Which groups are kept, from the experts' values.  A group is shared by as many lanes as there are for it, a power of two;
+// its place is the number of groups before it.
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, const WaveLds& sh) {
+  const int lane = threadIdx.x & 63, size = a.group_size.d;
+  const int share_log = a.groups > 32 ? 0 : 31 - __builtin_clz(64 / a.groups), share = 1 << share_log;
+  for (int g = lane >> share_log; g < a.groups; g += 64 >> share_log) {   // a group's lanes walk together
+    double first = kClosed, second = kClosed;
+    const auto fold = [&](double f, double o) {
+      second = max64(max64(second, o), min64(first, f));
+      first = max64(first, f);
+    };
+    for (int j = lane & (share - 1); j < size; j += share) fold(sh.value[g * size + j], kClosed);
+    if (share > 1) fold(row_dpp<kXor1>(first), row_dpp<kXor1>(second));
+    if (share > 2) fold(row_dpp<kXor2>(first), row_dpp<kXor2>(second));
+    if (share > 4) fold(row_dpp<kXor4>(first), row_dpp<kXor4>(second));
+    if (share > 8) fold(row_dpp<kXor8>(first), row_dpp<kXor8>(second));
+    if (share > 16) {   // two groups: all lanes are here
+      const Two f = rows_of_two(first), s = rows_of_two(second);
+      first = f.a, second = s.a;
+      fold(f.b, s.b);
+    }
+    double rank = first;
+    if (a.group_top == 2 && second != kClosed) rank = !a.bias && second == kNaN ? kNaN : first + second;
+    if (!(lane & (share - 1))) sh.rank[g] = rank;
+  }
+  wave_sync();
+  for (int g = lane; g < a.groups; g += 64) {
+    const double mine = sh.rank[g];
+    int before = 0;
+    for (int o = 0; o < a.groups; o++) before += sh.rank[o] > mine || (sh.rank[o] == mine && o < g);
+    sh.kept[g] = before < a.top_groups;
+  }
+  wave_sync();
+}
+
+// kOwn experts a lane: lane + 64 i.  4096 fp32 tokens of 128 experts, 20 of them chosen: 11.4 us.
+template <bool kBf16, int kOwn>
 __device__ void route_exact(const RouteArgs& a, int64_t token, char* lds) {
   const WaveLds sh(lds, a);
   const int lane = threadIdx.x & 63;
   const bool open = !a.mask || a.mask[token];
+  const bool sums = a.groups > 1 && a.group_top == 2;   // groups rank by scores
+  const bool scores = a.bias || sums;
   const char* const row = logit_row<kBf16>(a.logits, a.ld, token);
-  double l[kPer], p[kPer], key[kPer];
+  double key[kOwn];
   double top = kClosed, sum = 0;
+  {
+    double l[kOwn], p[kOwn], bias[kOwn];
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    const int e = lane + 64 * i;
-    l[i] = open && e < a.experts ? (double)logit_at<kBf16>(row, e) : kClosed;
-    top = fmax(top, l[i]);
-  }
-  top = wave_max(top);
-  if (top == kClosed) top = 0;
+    for (int i = 0; i < kOwn; i++) {
+      const int e = lane + 64 * i;
+      const float v = e < a.experts ? logit_at<kBf16>(row, e) : -kInf;
+      bias[i] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+      l[i] = open ? (double)v : kClosed;
+      if (e < a.experts) sh.logit[e] = v;
+    }
+    if (!a.sigmoid && (scores || !a.renormalize)) {
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    if (64 * i >= a.experts) continue;
-    p[i] = exp(a.sigmoid ? -l[i] : l[i] - top);
-    if (a.sigmoid) p[i] = 1 / (1 + p[i]);
-    else sum += p[i];
-  }
-  sum = a.sigmoid ? 1.0 : wave_add(sum);
+      for (int i = 0; i < kOwn; i++) top = fmax(top, l[i]);
+      top = wave_max(top);
+      if (top == kClosed) top = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    const int e = lane + 64 * i;
-    key[i] = l[i];
-    if (e >= a.experts) continue;
-    if (!a.sigmoid) p[i] /= sum;
-    if (a.bias && l[i] != kClosed) key[i] = p[i] + (double)a.bias[e];
-    if (key[i] != key[i]) key[i] = kNaN;
-    sh.key[e] = key[i];
-    sh.value[e] = a.bias ? key[i] : p[i];
+      for (int i = 0; i < kOwn; i++) {
+        p[i] = exp(l[i] - top);
+        sum += p[i];
+      }
+      sum = wave_add(sum);
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; i++) {
+      const int e = lane + 64 * i;
+      if (scores) p[i] = a.sigmoid ? 1 / (1 + exp(-l[i])) : p[i] / sum;
+      key[i] = a.bias && l[i] != kClosed ? p[i] + bias[i] : l[i];
+      if (key[i] != key[i]) key[i] = kNaN;
+      double v = key[i];
+      if (sums && !a.bias && v != kClosed) v = p[i] == p[i] ? p[i] : kNaN;
+      if (e < a.experts) sh.value[e] = v;
+    }
   }
   wave_sync();
   if (a.groups > 1) {
-    const int size = a.group_size.d;
-    double rank[kPer];
+    keep_groups(a, sh);
 #pragma unroll
-    for (int i = 0; i < kPer; i++) {
-      const int g = lane + 64 * i;
-      rank[i] = kClosed;
-      if (g < a.groups) {
-        double first = kClosed, second = kClosed, v1 = 0, v2 = 0;
-#pragma unroll 4
-        for (int j = 0; j < size; j++) {
-          const double k = sh.key[g * size + j], v = sh.value[g * size + j];
-          if (k > first) second = first, v2 = v1, first = k, v1 = v;
-          else if (k > second) second = k, v2 = v;
-        }
-        rank[i] = a.group_top == 1 || first == kClosed ? first : v1 + (second == kClosed ? 0.0 : v2);
-        if (rank[i] != rank[i]) rank[i] = kNaN;
-        sh.kept[g] = 0;
-      }
-    }
-    wave_sync();
-    for (int j = 0; j < a.top_groups; j++) {
-      const Best b = best_of(rank, a.groups);
-      if (b.key == kClosed) break;
-      take(rank, b.at);
-      if (lane == 0) sh.kept[b.at] = 1;
-    }
-    wave_sync();
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
+    for (int i = 0; i < kOwn; i++) {
       const int e = lane + 64 * i;
       if (e < a.experts && !sh.kept[mxq_quot((uint32_t)e, a.group_size)]) key[i] = kClosed;
     }
   }
-  for (int j = 0; j < a.top_k; j++) {
-    const Best b = best_of(key, a.experts);
-    take(key, b.at);
-    if (lane == 0) sh.chosen[j] = b.key == kClosed ? -1 : b.at;
+  for (int j = 0; j < a.top_k; j++) {   // the largest, the lowest index where several are equal
+    double most = key[0];
+#pragma unroll
+    for (int i = 1; i < kOwn; i++) most = max64(most, key[i]);
+    most = wave_fold(most, [](double a, double b) { return max64(a, b); });
+    int at = -1;
+#pragma unroll
+    for (int i = kOwn - 1; i >= 0; i--) {
+      const uint64_t equal = __ballot(key[i] == most && most != kClosed);
+      if (equal) at = 64 * i + __builtin_ctzll(equal);
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; i++)
+      if (lane + 64 * i == at) key[i] = kClosed;
+    if (lane == 0) sh.chosen[j] = at;
   }
   wave_sync();
   // weights: relative to the largest of the chosen logits where they are made to sum to scale
-  double largest = kClosed;
+  double largest = kClosed, total = 0;
+  if (a.renormalize) {
+    for (int j = lane; j < a.top_k; j += 64)
+      if (sh.chosen[j] >= 0) largest = fmax(largest, (double)sh.logit[sh.chosen[j]]);
+    largest = wave_max(largest);
+  }
   for (int j = lane; j < a.top_k; j += 64) {
     const int e = sh.chosen[j];
-    if (e >= 0) largest = fmax(largest, (double)logit_at<kBf16>(row, e));
+    const double v = e < 0 ? kClosed : (double)sh.logit[e];
+    double w;
+    if (!a.sigmoid) {
+      w = a.renormalize ? exp(v - largest) : exp(v - top) / sum;
+    } else {
+      const double m = a.renormalize ? fmin(largest, 0.0) : 0.0;
+      w = v > 0 ? exp(-m) / (1 + exp(-v)) : exp(v - m) / (1 + exp(v));
+    }
+    if (e < 0) w = 0;
+    sh.value[j] = w;   // the values have been used
+    total += w;
   }
-  largest = wave_max(largest);
-  const auto weight = [&](int e) -> double {
-    if (e < 0) return 0.0;
-    const double v = logit_at<kBf16>(row, e);
-    if (!a.sigmoid) return a.renormalize ? exp(v - largest) : exp(v - top) / sum;
-    const double m = a.renormalize ? fmin(largest, 0.0) : 0.0;
-    return v > 0 ? exp(-m) / (1 + exp(-v)) : exp(v - m) / (1 + exp(v));
-  };
-  double total = 0;
-  for (int j = lane; j < a.top_k; j += 64) total += weight(sh.chosen[j]);
-  total = wave_add(total);
-  const double scale = a.scale / (a.renormalize && total != 0 ? total : 1.0);
+  const double scale = a.scale / (a.renormalize ? [](double t) { return t != 0 ? t : 1.0; }(wave_add(total)) : 1.0);
   for (int j = lane; j < a.top_k; j += 64) {
     a.ids[token * a.top_k + j] = sh.chosen[j];
-    a.weights[token * a.top_k + j] = (float)(weight(sh.chosen[j]) * scale);
+    a.weights[token * a.top_k + j] = (float)(sh.value[j] * scale);
   }
   wave_sync();   // the LDS may take another token
 }
 
-template <bool kBf16>
+template <bool kBf16, int kOwn>
 __global__ __launch_bounds__(kThreads) void route_wave_kernel(RouteArgs a) {
   extern __shared__ __align__(16) char lds[];
   const int64_t token = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
-  if (token < a.tokens) route_exact<kBf16>(a, token, lds);
+  if (token < a.tokens) route_exact<kBf16, kOwn>(a, token, lds);
 }
 
 // ---- sixteen lanes to a token ------------------------------------------------------------
 // Keys are taken in fp32 first, which without a bias is what they are.  A biased score, or the sum of two scores that ranks
-// a group, is known to within a bound; where two that are told apart lie nearer than that, the wave takes its four tokens
-// again in 64 bits, and a token that even so has two within the bound (or a key that is not finite) as above.
+// a group, is known to within a bound.  Where two chosen experts, or the last of them and one that is left out, or two
+// groups lie nearer than that, the few in question are put in order by their keys in 64 bits, a lane each; where they are
+// not few, or a key is not finite, the wave takes the token as above.  All of the wave's tokens again in 64 bits took 16.0 us
+// where this takes 14.0, and that has about one token in a thousand in question.
 //
 // A key and its expert are one double: the key with the expert's index in the lowest nine bits, so that equal keys fall
 // by index and a comparison moves both.  Each lane sorts its own, and four exchanges between lanes leave the token's
@@ -306,15 +326,9 @@ __device__ __forceinline__ F row_add(F v) {
 }
 __device__ __forceinline__ bool row_any(bool v) { return row_max(v ? 1.0f : 0.0f) != 0; }
 
-// Of two numbers (none of these is a NaN, so nothing needs to be made quiet first).
-__device__ __forceinline__ double max64(double a, double b) {
-  double r;
-  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-  return r;
-}
 __device__ __forceinline__ void order(double& a, double& b) {
   const double x = max64(a, b);
-  asm("v_min_f64 %0, %1, %2" : "=v"(b) : "v"(a), "v"(b));
+  b = min64(a, b);
   a = x;
 }
 
@@ -343,13 +357,11 @@ __device__ __forceinline__ void sort_falling(double* v) {
 
 constexpr double kOpen = -0x1p995, kShut = -0x1p1000;   // open keys lie above kOpen
 
-// kExact: the key's lowest nine bits are 0, as those of an fp32 value.  An infinite key above makes a NaN, whose token is in
-// doubt anyway.
-template <bool kExact>
+// The key is an fp32 value, its lowest nine bits are 0.  An infinite key makes a NaN, whose token is in doubt anyway.
 __device__ __forceinline__ double with_index(double key, int e) {
   u32x2 b = __builtin_bit_cast(u32x2, max64(key, kShut));
   const uint32_t at = (uint32_t)(kMost - 1 - e) ^ ((uint32_t)((int)b[1] >> 31) & (kMost - 1));   // e itself below 0
-  b[0] = (kExact ? b[0] : b[0] & ~(uint32_t)(kMost - 1)) | at;
+  b[0] |= at;
   return __builtin_bit_cast(double, b);
 }
 __device__ __forceinline__ int index_of(double v) {
@@ -401,23 +413,12 @@ __device__ __forceinline__ int groups_before(F v, int g, int group_lanes) {
   return before;
 }
 
-// How scores are computed in fp32 and in 64 bits, and how far two of them may be off together: a sigmoid by 4 steps of 1 each, a
-// softmax by its up to 36 roundings of the sum, in parts of the largest score; a key by its own rounding and, in 64 bits, by
-// the nine bits of the index.
-template <typename F>
-struct Score;
-template <>
-struct Score<float> {
-  static constexpr float kSigmoid = 0x1p-20f, kSoftmax = 0x1p-17f, kKey = 0x1p-22f, kInfinite = __builtin_inff();
-  static __device__ __forceinline__ float exponential(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
-  static __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
-};
-template <>
-struct Score<double> {
-  static constexpr double kSigmoid = 0x1p-49, kSoftmax = 0x1p-46, kKey = 0x1p-41, kInfinite = __builtin_inf();
-  static __device__ __forceinline__ double exponential(double v) { return exp(v); }
-  static __device__ __forceinline__ double inverse(double v) { return 1 / v; }
-};
+// How far two scores in fp32 may be off together.  A sigmoid is off by 2^-23 for each of exp2 and the reciprocal, half of
+// that for the sum and, with p (1 - p) |x| < 0.23, by a fifth of it for the exponent: less than 2^-22 each.  A softmax is off
+// in parts of the largest score: the sum by 36 roundings and by its terms, 2.5 |z| + 2 of 2^-24 each with a weighted mean of
+// |z| < log 512, and the scores' own places: 62 of 2^-24 at most.  A key adds its own rounding, in parts of itself.
+constexpr float kSigmoidOff = 0x1p-21f, kSoftmaxOff = 0x1p-18f, kKeyOff = 0x1p-22f;
+__device__ __forceinline__ float exponential(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
 
 // A lane's experts: base, base + 1, ...; x their logits, -inf where there is none or it is closed; bias theirs.
 template <int kEach>
@@ -426,68 +427,185 @@ struct Mine {
   float x[kEach], bias[kEach];
 };
 
-// Lane j's pick, the token's j-th expert with its key, into *pick.  Returns whether the choice is in doubt.
-template <typename F, int kList, int kEach>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m, float top, double* pick) {
-  using S = Score<F>;
+// What lane j knows of its token's j-th expert.
+struct Pick {
+  int expert;
+  bool has;
+};
+
+// The experts for which near(i) holds, i of this lane's, into the token's place in LDS, up to 16 of them.  Returns how many.
+template <int kEach, typename F>
+__device__ __forceinline__ int list_near(const Mine<kEach>& m, int* list, F near) {
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; i++) {
+    const bool it = near(i);
+    const uint32_t all = (uint32_t)(__ballot(it) >> (threadIdx.x & 48)) & 0xFFFFu;   // of the token's lanes
+    const int at = count + __builtin_popcount(all & ((1u << m.lane16) - 1));
+    if (it && at < 16) list[at] = m.base + i;
+    count += __builtin_popcount(all);
+  }
+  wave_sync();
+  return count;
+}
+
+// In 64 bits: what divides a token's scores, and an expert's key (or score, where there is no bias).
+template <bool kBf16>
+__device__ __forceinline__ double sum_of_scores(const RouteArgs& a, const char* row, float top) {
+  if (a.sigmoid) return 1;
+  double sum = 0;
+#pragma unroll 1
+  for (int e = threadIdx.x & 15; e < a.experts; e += 16) sum += exp((double)logit_at<kBf16>(row, e) - (double)top);
+  return row_add(sum);
+}
+template <bool kBf16>
+__device__ __forceinline__ double key_of(const RouteArgs& a, const char* row, float top, double sum, int e) {
+  const double l = logit_at<kBf16>(row, e), t = exp(a.sigmoid ? -l : l - (double)top);
+  return (a.sigmoid ? 1 / (1 + t) : t / sum) + (a.bias ? (double)a.bias[e] : 0.0);
+}
+
+// f for the other lanes of the row, each N lanes away.
+template <int N = 1, typename F>
+__device__ __forceinline__ void for_others(F f) {
+  if constexpr (N < 16) {
+    f(std::integral_constant<int, 0x120 + N>{});
+    for_others<N + 1>(f);
+  }
+}
+
+// The groups in question (asked), put in order by values in 64 bits: the best of them are kept, as many as there is room
+// for.  Of a group's experts those whose values lie at `floor` or above can be its first two.  Returns whether these are
+// more than 16 for the token.
+template <bool kBf16, int kEach>
+__device__ __forceinline__ bool settle_groups(const RouteArgs& a, const Mine<kEach>& m, const char* row, float top,
+                                              const float (&value)[kEach], float floor, bool asked, int room, int* list,
+                                              bool* kept) {
+  const int count = list_near(m, list, [&](int i) { return asked && value[i] >= floor && value[i] > -kInf; });
+  const double sum = sum_of_scores<kBf16>(a, row, top);
+  const bool mine = m.lane16 < count;
+  const int e = mine ? list[m.lane16] : kMost, g = mine ? (int)mxq_quot((uint32_t)e, a.group_size) : -1 - m.lane16;
+  const double key = mine ? key_of<kBf16>(a, row, top, sum, e) : kClosed;
+  double first = key, second = kClosed;
+  bool leads = mine;   // one lane speaks for its group
+  for_others([&](auto ctrl) {
+    const double o = row_dpp<ctrl.value>(key);
+    const int og = (int)dpp<ctrl.value>((uint32_t)g), oe = (int)dpp<ctrl.value>((uint32_t)e);
+    if (og == g) {
+      second = fmax(second, fmin(first, o));
+      first = fmax(first, o);
+      leads &= !(o > key || (o == key && oe < e));
+    }
+  });
+  const double rank = a.group_top == 2 && second != kClosed ? first + second : first;
+  int before = 0;
+  for_others([&](auto ctrl) {
+    const double o = row_dpp<ctrl.value>(rank);
+    const int og = (int)dpp<ctrl.value>((uint32_t)g);
+    before += dpp<ctrl.value>((uint32_t)leads) && (o > rank || (o == rank && og < g));
+  });
+  wave_sync();
+  list[m.lane16] = 0;
+  wave_sync();
+  if (leads) list[g] = before < room;
+  wave_sync();
+  *kept = list[m.group] != 0;
+  wave_sync();
+  return count > 16;
+}
+
+// The experts whose keys lie at `edge` or above, put in order by their keys in 64 bits, a lane each.  Returns whether they
+// are more than that.
+template <bool kBf16, int kEach>
+__device__ __forceinline__ bool settle(const RouteArgs& a, const Mine<kEach>& m, const char* row, float top, bool kept,
+                                       const float (&key)[kEach], float edge, int* list, Pick* pick) {
+  // the edge itself may lie beyond the largest number
+  const int count = list_near(m, list, [&](int i) { return kept && key[i] >= edge && key[i] > -kInf; });
+  const double sum = sum_of_scores<kBf16>(a, row, top);
+  const bool mine = m.lane16 < count;
+  const int e = mine ? list[m.lane16] : kMost + m.lane16;
+  const int place = groups_before<1>(mine ? key_of<kBf16>(a, row, top, sum, e) : kClosed, e, 1);
+  wave_sync();
+  list[place] = e;
+  wave_sync();
+  *pick = Pick{list[m.lane16], mine && m.lane16 < a.top_k};
+  wave_sync();
+  return count > 16;
+}
+
+// Lane j's pick, the token's j-th expert, into *pick.  Returns whether the choice is in doubt.
+template <bool kBf16, int kList, int kEach>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m, const char* row, float top, int* list,
+                                       Pick* pick) {
   const bool sums = a.groups > 1 && a.group_top == 2;      // groups rank by scores
   bool doubt = false;
-  F s[kEach], bound = S::kSigmoid;
+  float s[kEach], bound = kSigmoidOff;
   if (a.bias || sums) {
     if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < kEach; i++) s[i] = S::inverse(1 + S::exponential(-(F)m.x[i]));
+      for (int i = 0; i < kEach; i++) s[i] = __builtin_amdgcn_rcpf(1 + exponential(-m.x[i]));
     } else {
-      F sum = 0;
+      float sum = 0;
 #pragma unroll
       for (int i = 0; i < kEach; i++) {
-        s[i] = S::exponential((F)m.x[i] - (F)top);
+        s[i] = exponential(m.x[i] - top);
         sum += s[i];
       }
       sum = row_add(sum);
-      const F r = sum > 0 ? 1 / sum : (F)0;
-      bound = S::kSoftmax * r;
+      const float r = sum > 0 ? 1 / sum : 0.0f;
+      bound = kSoftmaxOff * r;
 #pragma unroll
       for (int i = 0; i < kEach; i++) s[i] *= r;
     }
   }
-  F key[kEach];
+  float key[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; i++) {
     key[i] = m.x[i];
     if (a.bias) {
-      key[i] = m.x[i] == -kInf ? -S::kInfinite : s[i] + (F)m.bias[i];
-      doubt |= !(key[i] < S::kInfinite);
+      key[i] = m.x[i] == -kInf ? -kInf : s[i] + m.bias[i];
+      doubt |= !(key[i] < kInf);
     }
   }
   bool kept = true;
   if (a.groups > 1) {
     const int lanes = 1 << a.group_lanes_log;
-    F first = -S::kInfinite, second = first;
+    float value[kEach], first = -kInf, second = first;
 #pragma unroll
     for (int i = 0; i < kEach; i++) {
-      const F v = sums && !a.bias ? (m.x[i] == -kInf ? -S::kInfinite : s[i]) : key[i];
-      second = fmax(second, fmin(first, v));
-      first = fmax(first, v);
+      value[i] = sums && !a.bias ? (m.x[i] == -kInf ? -kInf : s[i]) : key[i];
+      second = fmaxf(second, fminf(first, value[i]));
+      first = fmaxf(first, value[i]);
     }
-    const auto fold = [&](F f, F o) {
-      second = fmax(fmax(second, o), fmin(first, f));
-      first = fmax(first, f);
+    const auto fold = [&](float f, float o) {
+      second = fmaxf(fmaxf(second, o), fminf(first, f));
+      first = fmaxf(first, f);
     };
     if (lanes > 1) fold(row_dpp<kXor1>(first), row_dpp<kXor1>(second));
     if (lanes > 2) fold(row_dpp<kXor2>(first), row_dpp<kXor2>(second));
     if (lanes > 4) fold(row_dpp<kXor4>(first), row_dpp<kXor4>(second));
-    const F rank = sums && second != -S::kInfinite ? first + second : first;
+    const float rank = sums && second != -kInf ? first + second : first;
     kept = groups_before<1>(rank, m.group, lanes) < a.top_groups;
     if (a.bias || sums) {
-      const F least = row_min(kept ? rank : S::kInfinite), most = row_max(kept ? -S::kInfinite : rank);
-      doubt |= most > -S::kInfinite && !(least - most >= 2 * bound + (fabs(least) + fabs(most)) * S::kKey);
+      doubt |= rank == -kInf && first != -kInf;   // a sum beyond the largest number
+      const float least = row_min(kept ? rank : kInf), most = row_max(kept ? -kInf : rank);
+      const float gap = kept ? rank - most : least - rank;
+      const bool asked = most > -kInf && !(gap >= 2 * bound + (fabsf(rank) + fabsf(kept ? most : least)) * kKeyOff);
+      const bool near = row_any(asked);
+      if (__any(near)) {
+        const float last = a.group_top == 2 ? second : first;
+        const int sure = (int)row_add(kept && !asked ? 1.0f : 0.0f) >> a.group_lanes_log;
+        bool settled;
+        const bool many = settle_groups<kBf16>(a, m, row, top, value, last - bound - fabsf(last) * kKeyOff, asked,
+                                               a.top_groups - sure, list, &settled);
+        if (asked) kept = settled;
+        doubt |= near && many;
+      }
     }
   }
   double d[kEach], v[kList];
 #pragma unroll
   for (int i = 0; i < kEach; i++)   // + 0: of the zeros one is as good as the other
-    d[i] = with_index<sizeof(F) == 4>(kept ? (double)(key[i] + 0) : -S::kInfinite, min(m.base + i, kMost - 1));
+    d[i] = with_index(kept ? (double)(key[i] + 0) : kClosed, min(m.base + i, kMost - 1));
   largest_of<kEach, kList>(d, v);
   merge_lanes<kXor1>(v);
   merge_lanes<kXor2>(v);
@@ -496,20 +614,26 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m,
   double mine = v[0];
 #pragma unroll
   for (int j = 1; j < kList; j++) mine = m.lane16 == j ? v[j] : mine;
-  *pick = mine;
+  *pick = Pick{index_of(mine), m.lane16 < a.top_k && mine > kOpen};
+  doubt = row_any(doubt);
   if (a.bias) {
-    const bool has = m.lane16 < a.top_k && mine > kOpen;
-    const F k = (F)mine, next = (F)row_dpp<0x101>(mine);   // of the next lane
-    const F step = bound + fabs(k) * S::kKey;
-    doubt |= has && m.lane16 + 1 < a.top_k && next > (F)kOpen && k - next < step;
+    const float k = (float)mine, next = (float)row_dpp<0x101>(mine);   // of the next lane
+    const float step = bound + fabsf(k) * kKeyOff;
+    bool near = pick->has && m.lane16 + 1 < a.top_k && next > (float)kOpen && k - next < step;
     // and the last of them against those that are left out: how many keys lie above it less the step
-    const F edge = row_min(has ? k - step : S::kInfinite);
+    const float edge = row_min(pick->has ? k - step : kInf);
     int above = 0;
 #pragma unroll
     for (int i = 0; i < kEach; i++) above += kept && key[i] >= edge;
-    doubt |= row_add((float)above) > (float)a.top_k;
+    near |= row_add((float)above) > (float)a.top_k;
+    near = row_any(near) && !doubt;
+    if (__any(near)) {
+      Pick settled;
+      const bool many = settle<kBf16>(a, m, row, top, kept, key, edge, list, &settled);
+      if (near) *pick = settled, doubt = many;
+    }
   }
-  return row_any(doubt);
+  return doubt;
 }
 
 // A lane's row of experts, kAt of them in 16 bytes; those from `count` on -inf.
@@ -531,6 +655,7 @@ template <int kEach, int kList, bool kBf16>
 __global__ __launch_bounds__(kThreads) void route_row_kernel(RouteArgs a) {
   keep_denormals();
   extern __shared__ __align__(16) char lds[];
+  __shared__ int lists[kThreads / 16][16];
   Mine<kEach> m;
   m.lane16 = threadIdx.x & 15;
   const int64_t token = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
@@ -558,12 +683,10 @@ __global__ __launch_bounds__(kThreads) void route_row_kernel(RouteArgs a) {
   top = row_max(top);
   const bool odd = !(top < kInf);   // a NaN or +Inf among the logits
   if (top == -kInf) top = 0;
-  double mine;
-  bool again = choose<float, kList>(a, m, top, &mine) && !odd;
-  if (__any(again)) again = choose<double, kList>(a, m, top, &mine) && again;
-  again = (again || odd) && open;
-  const bool has = m.lane16 < a.top_k && mine > kOpen;
-  const int e = index_of(mine);
+  Pick pick;
+  const bool again = (choose<kBf16, kList>(a, m, row, top, lists[threadIdx.x / 16], &pick) || odd) && open;
+  const bool has = pick.has;
+  const int e = pick.expert;
   const float l = has ? logit_at<kBf16>(row, min(e, a.experts - 1)) : -kInf;
   float w = 0;
   if (a.renormalize) {
@@ -584,7 +707,7 @@ __global__ __launch_bounds__(kThreads) void route_row_kernel(RouteArgs a) {
   } else {
     float sum = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; i++) sum += Score<float>::exponential(m.x[i] - top);
+    for (int i = 0; i < kEach; i++) sum += exponential(m.x[i] - top);
     sum = row_add(sum);
     w = has ? expf(l - top) / sum : 0.0f;
   }
@@ -595,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void route_row_kernel(RouteArgs a) {
   // the tokens that are still in doubt, one after the other
   for (uint64_t left = __ballot(again && m.lane16 == 0); left; left &= left - 1) {
     const int64_t first = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 64 * 4;
-    route_exact<kBf16>(a, first + __builtin_ctzll(left) / 16, lds);
+    route_exact<kBf16, kEach / 4>(a, first + __builtin_ctzll(left) / 16, lds);
   }
 }
 
@@ -801,7 +924,9 @@ int launch_route(RouteArgs a, hipStream_t stream) {
   const size_t lds = kThreads / 64 * WaveLds::bytes(a.experts, a.top_k, a.groups);
   // groups of whole lanes: 1, 2, 4, 8 or 16 of them
   if (a.groups > 16 || (a.groups & (a.groups - 1)) || a.top_k > kListMost)
-    return launch_tokens(a, 64, from, route_wave_kernel<kBf16>, lds, stream);
+    return a.experts <= 128   ? launch_tokens(a, 64, from, route_wave_kernel<kBf16, 2>, lds, stream)
+           : a.experts <= 256 ? launch_tokens(a, 64, from, route_wave_kernel<kBf16, 4>, lds, stream)
+                              : launch_tokens(a, 64, from, route_wave_kernel<kBf16, 8>, lds, stream);
   const int size = a.experts / a.groups, lanes = 16 / a.groups;
   a.group_lanes_log = __builtin_ctz(lanes);
   a.per = (size + lanes - 1) / lanes;

@@ -126,6 +126,50 @@ def test_route_scores_next_to_each_other():
     check(torch.linspace(30, 90, E)[None].repeat(3, 1), 6, score="sigmoid", bias=torch.zeros(E))  # by the scores: many are 1
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (256, 16), (96, 6), (32, 2), (512, 4), (80, 16)])
+def test_route_few_next_to_each_other(E, groups, score):
+    """Clusters of 2 to 20 keys, or of two groups, that fp32 does not tell apart, and nothing else near: at the last choice, before
+    it and behind it.  The keys of a token differ from the first token's by a few steps of fp32."""
+    g = gen(E + groups)
+    l = (0.5 * torch.randn(1, E, generator=g)).repeat(40, 1)
+    p = torch.tensor(ref.scores(l[:1], score), dtype=torch.float64)[0]
+    l[1:] += torch.randint(-2, 3, (39, E), generator=g) * 2.0 ** -22
+    mask = torch.arange(40) % 7 != 3
+    for cluster in (2, 15, 16, 17, 20):
+        place = torch.empty(E, dtype=torch.long)
+        place[torch.randperm(E, generator=g)] = torch.arange(E) // cluster
+        bias = (1 + 0.02 * place - p).float()
+        for k in (1, 7, 15):
+            check(l, k, score=score, bias=bias, mask=mask)
+    size = E // groups
+    for width in (2, groups):
+        inside = torch.rand(E // groups, generator=g).repeat(groups)          # the groups of a cluster are alike
+        bias = (1 + 0.02 * (torch.arange(E) // size // width) + 0.3 * inside - p).float()
+        for top in (1, (groups + 1) // 2):
+            for group_top in (1, 2):
+                check(l, min(5, size), score=score, bias=bias, mask=mask, n_groups=groups, top_groups=top, group_top=group_top)
+    if score == "sigmoid":   # groups of equal logits, which rank by their scores
+        l = l.view(40, groups, size)[:, :1].repeat(1, groups, 1) + torch.randint(-2, 3, (40, groups, size), generator=g) * 2.0 ** -22
+        check(l.reshape(40, E), min(5, size), score=score, n_groups=groups, top_groups=(groups + 1) // 2, group_top=2)
+
+
+def test_route_biases_of_the_lowest_value():
+    """Experts that a bias of about the lowest number puts last, also in groups whose two add up to less than that."""
+    g = gen(21)
+    E, low = 64, torch.finfo(FP32).min
+    l = logits_of(30, E, 22)
+    l[3:6, 5:20] = -INF
+    for score in ("softmax", "sigmoid"):
+        for part in (slice(8, 60), slice(0, 64), slice(17, 24)):
+            bias = 0.1 * torch.randn(E, generator=g)
+            bias[part] = low * (1 - 0.25 * torch.rand(E, generator=g)[part])
+            bias[20:26] = low
+            for k, how in ((8, {}), (20, {}), (8, {"n_groups": 8, "top_groups": 5, "group_top": 2}), (6, {"n_groups": 8, "top_groups": 2}),
+                           (3, {"n_groups": 16, "top_groups": 9, "group_top": 2})):
+                check(l, k, score=score, bias=bias, **how)
+
+
 def test_route_values_that_are_not_finite():
     """A NaN is chosen last of those that are open; +Inf first; nothing else of the batch changes."""
     l = logits_of(20, 40, 11)
