@@ -70,9 +70,10 @@ __device__ __forceinline__ float row_sum(float v, Meeting& m) {
   return lane_sum<16>(lane16 < kWaves ? m.part[lane16] : 0.0f);
 }
 
-__device__ __forceinline__ float add_squares(f32x8 s, float sum) {
+template <typename V>
+__device__ __forceinline__ float add_squares(V s, float sum) {
 #pragma unroll
-  for (int i = 0; i < kEPL; i++) sum = fmaf(s[i], s[i], sum);
+  for (int i = 0; i < (int)(sizeof(V) / 4); i++) sum = fmaf(s[i], s[i], sum);
   return sum;
 }
 
@@ -120,10 +121,56 @@ __global__ __launch_bounds__(kNormThreads<kLanes>) void norm_kernel(NormArgs a) 
   for (int i = 0; i < kChunks; i++) {
     const int c = (i * kLanes + lane) * kEPL;
     const f32x8 y = s[i] * r * weight_at<kVec>(a.weight, a.w_bf16, c, a.K);
-    // two stores of fp32 each fill half of a line, and the hint sends the halves out one by one: 8192 x 8192 fp32 210 -> 256 us
+    // two stores of fp32 each fill half of a line, and the hint sends the halves out one by one: 8192 x 8192 fp32
+    // of such pieces 210 -> 256 us
     if (a.sum) store_floats<TS, kVec, kStream && sizeof(TS) == 2>((TS*)a.sum + row * a.ld_sum, c, a.K, s[i]);
     if (a.y) store_floats<TX, kVec, kStream && sizeof(TX) == 2>((TX*)a.y + row * a.ld_y, c, a.K, y);
     if (a.data) store_group<kVec, kStream>(a.data + row * a.ld_data, a.scale + row * a.scale_ld, c, a.K, y);
+  }
+}
+
+// As norm_kernel, for fp32 rows at multiples of 16 bytes, with pieces of four elements: an instruction covers whole lines, and
+// the hint sends out whole ones.  8192 x 8192 fp32 with a residual and y 194 us, in pieces of eight 208; groups along both
+// of 4096 x 8192 99 for 111.  With a bf16 x beside an fp32 residual it is as fast either way.
+template <typename TS, int kLanes, int kChunks, bool kStream>
+__global__ __launch_bounds__(kNormThreads<kLanes>) void norm_four_kernel(NormArgs a) {
+  keep_denormals();
+  __shared__ Meeting meet[2];
+  static_assert(kLanes >= 64, "32 lanes hold a group");
+  const int64_t row = (int64_t)blockIdx.x * (kNormThreads<kLanes> / kLanes) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  if (row >= a.rows) return;   // a workgroup that meets at barriers has one row
+  f32x4 s[kChunks];
+  float sum = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; i++) {
+    const int c = (i * kLanes + lane) * 4;
+    s[i] = load_four<uint32_t, !kStream>((const float*)a.x + row * a.ld_x, c, a.K);
+    if (a.residual) s[i] += load_four<TS, !kStream>((const TS*)a.residual + row * a.ld_res, c, a.K);
+    if (a.residual && sizeof(TS) == 2) s[i] = widen4(narrow4(s[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; i++) sum = add_squares(s[i], sum);
+  sum = row_sum<kLanes>(sum, meet[0]);
+  float f = 1.0f;
+  if (!(sum < __builtin_inff())) {   // the same for the whole row
+    f = kDown;
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kChunks; i++) sum = add_squares(s[i] * kDown, sum);
+    sum = row_sum<kLanes>(sum, meet[1]);
+  }
+  const float r = inverse_root(sum, f, a.eps, a.K);
+  if (a.stats && lane == 0) a.stats[row] = r;
+#pragma unroll
+  for (int i = 0; i < kChunks; i++) {
+    const int c = (i * kLanes + lane) * 4;
+    f32x4 w{1, 1, 1, 1};
+    if (a.weight) w = a.w_bf16 ? load_four<uint16_t>(a.weight, c, a.K) : load_four<uint32_t>(a.weight, c, a.K);
+    const f32x4 y = s[i] * r * w;
+    if (a.sum) store_four<TS, kStream>((TS*)a.sum + row * a.ld_sum, c, a.K, s[i]);
+    if (a.y) store_four<uint32_t, kStream>((float*)a.y + row * a.ld_y, c, a.K, y);
+    if (a.data) store_group_four<kStream>(a.data + row * a.ld_data, a.scale + row * a.scale_ld, c, a.K, y);
   }
 }
 
@@ -214,7 +261,8 @@ struct BackRow {
 // A workgroup takes a row (as many as it has lanes for), and then every one as many rows further as the card works on at
 // once, the next row on its way while this one is worked out; it keeps its part of dw in registers.  8192 x 8192 bf16 96.5
 // us; 102.0 where each takes a run of neighbouring rows.  Loads with the non-temporal hint, stores without: so 99.9, plain
-// loads 113, stores with it as well 102.5, loads without and stores with it 109, all in such runs.
+// loads 113, stores with it as well 102.5, loads without and stores with it 109, all in such runs.  Of fp32 a load takes half
+// of each line and goes without it: 8192 x 8192 fp32 206.9 -> 197.9 us, bf16 beside an fp32 stream 178.9 -> 167.7.
 template <typename TY, typename TS, int kLanes, int kChunks, bool kVec>
 __global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) {
   keep_denormals();
@@ -235,9 +283,9 @@ __global__ __launch_bounds__(kNormThreads<kLanes>) void back_kernel(BackArgs a) 
 #pragma unroll
     for (int i = 0; i < kChunks; i++) {
       const int c = row < hi ? (i * kLanes + lane) * kEPL : a.K;
-      v.s[i] = load_chunk<TS, kVec, true>((const TS*)a.s + r * a.ld_s, c, a.K);
-      v.dy[i] = load_chunk<TY, kVec, true>((const TY*)a.dy + r * a.ld_dy, c, a.K);
-      if (a.dres) v.dres[i] = load_chunk<TS, kVec, true>((const TS*)a.dres + r * a.ld_dres, c, a.K);
+      v.s[i] = load_chunk<TS, kVec, sizeof(TS) == 2>((const TS*)a.s + r * a.ld_s, c, a.K);
+      v.dy[i] = load_chunk<TY, kVec, sizeof(TY) == 2>((const TY*)a.dy + r * a.ld_dy, c, a.K);
+      if (a.dres) v.dres[i] = load_chunk<TS, kVec, sizeof(TS) == 2>((const TS*)a.dres + r * a.ld_dres, c, a.K);
     }
   };
   int turn = 0;
@@ -439,11 +487,14 @@ NormArgs from_row(NormArgs a, int64_t r, int64_t n) {
 template <typename TX, typename TS, int kLanes, int kChunks, bool kVec, bool kStream>
 int launch_norm(const NormArgs& a, hipStream_t stream) {
   constexpr int threads = kNormThreads<kLanes>, per = threads / kLanes;
+  const auto kernel = [] {
+    if constexpr (sizeof(TX) == 4 && kVec && kLanes >= 64) return norm_four_kernel<TS, kLanes, 2 * kChunks, kStream>;
+    else return norm_kernel<TX, TS, kLanes, kChunks, kVec, kStream>;
+  }();
   const int64_t step = rows_per_launch(kLanes);
   for (int64_t r = 0; r < a.rows; r += step) {
     const int64_t n = std::min<int64_t>(step, a.rows - r);
-    hipLaunchKernelGGL((norm_kernel<TX, TS, kLanes, kChunks, kVec, kStream>), dim3((uint32_t)((n + per - 1) / per)),
-                       dim3(threads), 0, stream, from_row<TX, TS>(a, r, n));
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((n + per - 1) / per)), dim3(threads), 0, stream, from_row<TX, TS>(a, r, n));
     MXQ_TRY(launch_status());
   }
   return MXQ_OK;
