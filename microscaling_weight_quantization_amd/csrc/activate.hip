@@ -150,6 +150,7 @@ template <typename T, int kAct, bool kVec, bool kStream, bool kWhole, int kRows>
 __device__ __forceinline__ void act_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
                                          TileShared<kRows>& shared) {
   Chunk<uint32_t> v[kRows];
+  const int have = t.have();
   constexpr int kAtOnce = sizeof(T) == 2 ? kRows : kRows / 2;   // rows whose operands are on their way at once
   Walk<T, kVec, kVec && sizeof(T) == 2, false, kWhole, kGroup / kRows> walk(s, t, blockIdx.x * kGroup);
 #pragma unroll
@@ -158,7 +159,10 @@ __device__ __forceinline__ void act_tile(const ActArgs& s, const TileRows& t, in
 #pragma unroll
     for (int i = 0; i < kAtOnce; i++) walk.next(raw[i]);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; i++) v[i0 + i] = narrow<uint32_t>(value_of<T, kAct>(raw[i], s.up != nullptr));
+    for (int i = 0; i < kAtOnce; i++) {   // rows that there are not are not computed: 130 x 11904 of 56 experts 34.3 -> 18.8 us
+      v[i0 + i] = Chunk<uint32_t>{};
+      if (kWhole || kGroup / kRows * (i0 + i) < have) v[i0 + i] = narrow<uint32_t>(value_of<T, kAct>(raw[i], s.up != nullptr));
+    }
   }
   store_tile<uint32_t, kVec, true, kStream, kWhole>(v, out, t, id, blockIdx.x, shared);
 }
@@ -227,6 +231,7 @@ template <typename T, int kAct, bool kVec, bool kStream, Part kPart, bool kWhole
 __device__ __forceinline__ void act_backward_tile(const ActArgs& s, const TileRows& t, int id, const TileOut& out,
                                                   TileShared<kRows>& shared) {
   constexpr int kStep = kGroup / kRows;
+  const int have = t.have();
   Chunk<uint32_t> v[kRows], u[kPart == kBothHalves ? kRows : 1];
   if constexpr (kPart != kBorder) {
     constexpr int kAtOnce = sizeof(T) == 2 ? kRows : kRows / 2;   // rows whose operands are on their way at once
@@ -238,6 +243,11 @@ __device__ __forceinline__ void act_backward_tile(const ActArgs& s, const TileRo
       for (int i = 0; i < kAtOnce; i++) walk.next(raw[i]);
 #pragma unroll
       for (int i = 0; i < kAtOnce; i++) {
+        if (!kWhole && kStep * (i0 + i) >= have) {   // no such row
+          v[i0 + i] = Chunk<uint32_t>{};
+          if constexpr (kPart == kBothHalves) u[i0 + i] = Chunk<uint32_t>{};
+          continue;
+        }
         const Both b = gradients_of<T, kAct>(raw[i], s.up != nullptr);
         v[i0 + i] = narrow<uint32_t>(kPart == kUpHalf ? b.up : b.gate);
         if constexpr (kPart == kBothHalves) u[i0 + i] = narrow<uint32_t>(b.up);

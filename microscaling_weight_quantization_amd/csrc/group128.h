@@ -241,9 +241,11 @@ __device__ __forceinline__ void store_tile(const Chunk<T> (&v)[kRows], const Til
     uint32_t mine = 0;   // lane i of the 16 stores the code of their i-th row
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
-      const uint32_t code = code_of<T>(max16(v[i].amax()));
-      if (kWhole || row16 + kStep * i < have) store_chunk<kVec, kStream>(p, c, kWhole ? c + 1 : o.K, payload_of(v[i], code));
-      mine = lane16 == i ? code : mine;
+      if (kWhole || kStep * i < have) {   // the same for the whole workgroup
+        const uint32_t code = code_of<T>(max16(v[i].amax()));
+        if (kWhole || row16 + kStep * i < have) store_chunk<kVec, kStream>(p, c, kWhole ? c + 1 : o.K, payload_of(v[i], code));
+        mine = lane16 == i ? code : mine;
+      }
       p += kStep * o.ld_row;
     }
     const int r = row16 + kStep * lane16;
@@ -308,6 +310,7 @@ __device__ __forceinline__ void store_tile(const Chunk<T> (&v)[kRows], const Til
   // Two rows at a time: a conversion takes two values of one scale, so a column's pair of rows.
 #pragma unroll
   for (int i = 0; i < kRows; i += 2) {
+    if (!kWhole && kStep * i >= have) break;   // the same for the whole workgroup
     uint32_t pair[kEPL / 2];   // bytes: row i, row i + 1 of column 2 j, then of column 2 j + 1
 #pragma unroll
     for (int j = 0; j < kEPL / 2; j++) {
