@@ -10,7 +10,7 @@
 //
 // Memory bounds it; every element is read once.  2048 x 28672 bf16 by rows 47.2 us (294 MB, 6.2 TB/s, a plain copy's rate
 // being 6.6); both ways 128 rows x 128 columns a workgroup, of whose rows it touches 256 bytes each: 49152 x 1024 53.6 us
-// (303 MB, 5.6 TB/s), its gradients 97 (505 MB, 5.2), which two workgroups a CU hold in 170 registers a lane.
+// (303 MB, 5.6 TB/s), its gradients 97 (505 MB, 5.2), of which two workgroups fit a CU.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>

@@ -11,7 +11,7 @@
 //              where the weights sum to scale, p_j h_j = w_j (g_j - sum g w / scale), for both,
 //              and sum h p = 0
 //
-// Instructions bound the choice, about 1200 a wave of four tokens, most of them comparisons in pairs: 16384 fp32 tokens of 256
+// Instructions bound the choice, about 1250 a wave of four tokens, most of them comparisons in pairs: 16384 fp32 tokens of 256
 // experts with a bias and 8 groups 14.0 us, 131072 of them 63.6 (2.2 TB/s); 131072 bf16 tokens of 128 experts 27.5.
 // Gradients of 131072 bf16 tokens of 128 experts take 23.9 us, 6.0 TB/s.
 #include <hip/hip_runtime.h>
