@@ -416,7 +416,8 @@ __device__ __forceinline__ int groups_before(F v, int g, int group_lanes) {
 // How far two scores in fp32 may be off together.  A sigmoid is off by 2^-23 for each of exp2 and the reciprocal, half of
 // that for the sum and, with p (1 - p) |x| < 0.23, by a fifth of it for the exponent: less than 2^-22 each.  A softmax is off
 // in parts of the largest score: the sum by 36 roundings and by its terms, 2.5 |z| + 2 of 2^-24 each with a weighted mean of
-// |z| < log 512, and the scores' own places: 62 of 2^-24 at most.  A key adds its own rounding, in parts of itself.
+// |z| < log 512, and the scores' own places: 62 of 2^-24 at most.  A key adds its own rounding, in parts of itself, and so does
+// a sum of two keys, which is no larger than their magnitudes: 2^-24 of these for the keys and as much for the sum.
 constexpr float kSigmoidOff = 0x1p-21f, kSoftmaxOff = 0x1p-18f, kKeyOff = 0x1p-22f;
 __device__ __forceinline__ float exponential(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
 
@@ -583,13 +584,15 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Mine<kEach>& m,
     if (lanes > 1) fold(row_dpp<kXor1>(first), row_dpp<kXor1>(second));
     if (lanes > 2) fold(row_dpp<kXor2>(first), row_dpp<kXor2>(second));
     if (lanes > 4) fold(row_dpp<kXor4>(first), row_dpp<kXor4>(second));
-    const float rank = sums && second != -kInf ? first + second : first;
+    const bool two = sums && second != -kInf;
+    const float rank = two ? first + second : first;
     kept = groups_before<1>(rank, m.group, lanes) < a.top_groups;
     if (a.bias || sums) {
-      doubt |= rank == -kInf && first != -kInf;   // a sum beyond the largest number
-      const float least = row_min(kept ? rank : kInf), most = row_max(kept ? -kInf : rank);
-      const float gap = kept ? rank - most : least - rank;
-      const bool asked = most > -kInf && !(gap >= 2 * bound + (fabsf(rank) + fabsf(kept ? most : least)) * kKeyOff);
+      doubt |= fabsf(rank) == kInf && fabsf(first) != kInf;   // a sum beyond the largest number
+      // as far as the rank may be off: keys of opposite signs are rounded each in parts of itself, however small their sum is
+      const float off = first == -kInf ? 0.0f : bound + (fabsf(first) + (two ? fabsf(second) : 0.0f)) * kKeyOff;
+      const float least = row_min(kept ? rank - off : kInf), most = row_max(kept ? -kInf : rank + off);
+      const bool asked = most > -kInf && !(kept ? rank - off > most : rank + off < least);
       const bool near = row_any(asked);
       if (__any(near)) {
         const float last = a.group_top == 2 ? second : first;
