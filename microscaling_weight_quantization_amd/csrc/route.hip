@@ -781,12 +781,15 @@ __global__ __launch_bounds__(kThreads) void route_backward_wave_kernel(BackArgs 
     return v > 0 ? exp(-m) / (1 + exp(-v)) : exp(v - m) / (1 + exp(v));
   };
   double total = 0, dot = 0;
+  bool some = false;
   for (int j = lane; j < a.top_k; j += 64)
     if (chosen(j) >= 0) {
+      some = true;
       const double p = weight(chosen(j));
       total += p;
       dot += p * grads[j];
     }
+  const bool spread = dense && __any(some);   // of a token without a choice the gradient is 0, whatever the logits hold
   total = wave_add(total);
   dot = wave_add(dot);
   for (int j = lane; j < a.top_k; j += 64) {
@@ -804,7 +807,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_wave_kernel(BackArgs 
     const int e = lane + 64 * i;
     if (e >= a.experts) continue;
     double v = d[e];
-    if (dense) v -= exp(l[i] - top) / sum * dot * a.scale;
+    if (spread) v -= exp(l[i] - top) / sum * dot * a.scale;
     if constexpr (kBf16) ((__bf16*)out)[e] = (__bf16)(float)v;
     else ((float*)out)[e] = (float)v;
   }
@@ -825,6 +828,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(BackArgs a
   const bool dense = !a.sigmoid && !a.renormalize;
   const int32_t id = live && lane16 < a.top_k ? a.ids[token * a.top_k + lane16] : -1;
   const bool has = id >= 0 && id < a.experts;
+  const uint64_t chosen = __ballot(has);   // of the wave's four tokens
   const float grad = has ? a.dweights[token * a.top_k + lane16] : 0.0f;
   const float l = has ? logit_at<kBf16>(row, id) : -kInf;
   float x[kEach], top = -kInf, sum = 1.0f;
@@ -874,20 +878,22 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(BackArgs a
   if (has) atomicAdd(d + id, h * a.scale);   // one addition for each expert, unless ids names one twice
   wave_sync();
   if (!live) return;
-  const float less = dense ? dot * a.scale / sum : 0.0f;
+  // of a token without a choice the gradient is 0, whatever the logits hold
+  const bool spread = dense && (uint16_t)(chosen >> (threadIdx.x & 48)) != 0;
+  const float less = spread ? dot * a.scale / sum : 0.0f;
   char* const out = (char*)a.out + token * a.ld_out * (kBf16 ? 2 : 4);
 #pragma unroll
   for (int i = 0; i < kEach; i += kAt) {
     const int e = i * 16 + lane16 * kAt;
     if (e >= a.experts) continue;
     if constexpr (kAt == 1) {
-      const float v = dense ? d[e] - x[i] * less : d[e];
+      const float v = spread ? d[e] - x[i] * less : d[e];
       if constexpr (kBf16) ((__bf16*)out)[e] = (__bf16)v;
       else ((float*)out)[e] = v;
     } else {
       f32x8 v{};
 #pragma unroll
-      for (int j = 0; j < kAt; j++) v[j] = dense ? d[e + j] - x[i + j] * less : d[e + j];
+      for (int j = 0; j < kAt; j++) v[j] = spread ? d[e + j] - x[i + j] * less : d[e + j];
       const Chunk<uint16_t> b = narrow<uint16_t>(v);
       const u32x4 half{b.w[0], b.w[1], b.w[2], b.w[3]};
       const u32x8 full = __builtin_bit_cast(u32x8, v);
