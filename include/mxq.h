@@ -495,7 +495,7 @@ int mxq_mxfp4_packed_to_fp8_block128(const uint8_t* packed, const uint8_t* scale
  *            n_experts <= 512): expert e owns rows [offsets[e], offsets[e+1]),
  *            its groups begin at its first row, and scale is [rows/128 (rounded
  *            down) + n_experts, scale_ld], the experts' groups in order; code
- *            rows that no group needs are 0, and rows of no expert (from
+ *            rows that no group needs are 0 (also in a call on no rows), and rows of no expert (from
  *            offsets[n_experts] on, or before offsets[0]) have payload 0.  Offsets are taken as
  *            clamped to [0, rows] and to a rising order.
  *   data     [rows, K], row stride ld_data >= K;  scale_ld >= K

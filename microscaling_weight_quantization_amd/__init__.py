@@ -1214,6 +1214,7 @@ def _halves(gate: torch.Tensor, up: Optional[torch.Tensor], activation: str):
         if up.dtype != gate.dtype:
             raise ValueError(f"gate and up must have one dtype, got {gate.dtype} and {up.dtype}")
         pu, ldu = _same_rows(up, rows, F, "up")
+        pu = pu or 16                   # a tensor of no rows has no address, and none would stand for no second half
     return (pg, ldg, pu, ldu, rows, F, _float_code(gate), _named(_ACTIVATIONS, activation, "activation")), rows, F
 
 

@@ -418,9 +418,10 @@ int tile_entry(const ActArgs& a, int64_t rows, int64_t F, mxq_dtype dt, const in
   Operands in;
   bool empty;
   const int st = check_operands(a, rows, F, dt, backward, &in, &empty);
-  if (st != MXQ_OK || empty) return st;
-  if (!row_data || !row_scale || !col_data || !col_scale) return MXQ_ERR_NULL;
+  if (st != MXQ_OK) return st;
   const int64_t K = backward && a.up ? 2 * F : F;
+  if (empty) return offsets && rows == 0 ? clear_code_rows(col_scale, col_scale_ld, experts, K, offsets, stream) : MXQ_OK;
+  if (!row_data || !row_scale || !col_data || !col_scale) return MXQ_ERR_NULL;
   if (ld_row < K || row_scale_ld < groups_of(K) || ld_col < K || col_scale_ld < K) return MXQ_ERR_SHAPE;
   const int64_t code_rows = offsets ? rows / kGroup + experts : groups_of(rows);
   const Range rd = matrix_range(row_data, rows, K, ld_row, 1), rs = matrix_range(row_scale, rows, groups_of(K), row_scale_ld, 1),

@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "checks.h"
 #include "segments.h"
 
 namespace mxq_dev {
@@ -343,4 +344,28 @@ __device__ __forceinline__ bool whole_tile(const TileRows& t, int at, int K) {
   return t.hi - t.first >= kGroup && (at + 1) * kGroup <= K;
 }
 
+// A column a lane, a code row a workgroup's row.
+template <int kThreads>
+__global__ __launch_bounds__(kThreads) void clear_code_rows_kernel(uint8_t* scale, int64_t ld, int K) {
+  const int c = blockIdx.x * kThreads + threadIdx.x;
+  if (c < K) scale[blockIdx.y * ld + c] = 0;
+}
+
 }  // namespace mxq_dev
+
+namespace mxq_host {
+
+// A call by expert on no rows: its code rows, one an expert, are all ones that no group needs.  Without a place for them
+// there is nothing to do.
+template <int kThreads = 256>
+int clear_code_rows(uint8_t* scale, int64_t ld, int64_t experts, int64_t K, const int32_t* offsets, hipStream_t stream) {
+  if (!scale || K == 0) return MXQ_OK;
+  const Range rs = matrix_range(scale, experts, K, ld, 1), ro = matrix_range(offsets, 1, experts + 1, experts + 1, 4);
+  if (ld < K || !all_ok({rs, ro}) || !aligned(offsets, 4)) return MXQ_ERR_SHAPE;
+  if (overlap(rs, ro)) return MXQ_ERR_ALIAS;
+  const dim3 grid((uint32_t)((K + kThreads - 1) / kThreads), (uint32_t)experts);
+  hipLaunchKernelGGL((mxq_dev::clear_code_rows_kernel<kThreads>), grid, dim3(kThreads), 0, stream, scale, ld, (int)K);
+  return launch_status();
+}
+
+}  // namespace mxq_host

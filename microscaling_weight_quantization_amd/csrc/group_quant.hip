@@ -174,7 +174,8 @@ int tile_entry(const void* x, int64_t ld_x, int64_t x_rows, int64_t rows, int64_
   Checked c;
   bool empty;
   const int st = check_source(x, ld_x, x_rows, rows, K, dt, slots, top_k, offsets, experts, &c, &empty);
-  if (st != MXQ_OK || empty) return st;
+  if (st != MXQ_OK) return st;
+  if (empty) return offsets && rows == 0 ? clear_code_rows(col_scale, col_scale_ld, experts, K, offsets, stream) : MXQ_OK;
   if (!col_data || !col_scale || (row && (!row_data || !row_scale))) return MXQ_ERR_NULL;
   if (ld_col < K || col_scale_ld < K || (row && (ld_row < K || row_scale_ld < groups_of(K)))) return MXQ_ERR_SHAPE;
   const int64_t code_rows = offsets ? rows / kGroup + experts : groups_of(rows);
