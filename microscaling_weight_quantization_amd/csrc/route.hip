@@ -309,17 +309,8 @@ __device__ __forceinline__ double row_fold(double v, F f) {
 // A NaN stays.
 __device__ __forceinline__ float high(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float low(float a, float b) { return __builtin_elementwise_minimum(a, b); }
-// These do not meet one.
-__device__ __forceinline__ double high(double a, double b) { return fmax(a, b); }
-__device__ __forceinline__ double low(double a, double b) { return fmin(a, b); }
-template <typename F>
-__device__ __forceinline__ F row_max(F v) {
-  return row_fold(v, [](F a, F b) { return high(a, b); });
-}
-template <typename F>
-__device__ __forceinline__ F row_min(F v) {
-  return row_fold(v, [](F a, F b) { return low(a, b); });
-}
+__device__ __forceinline__ float row_max(float v) { return row_fold(v, high); }
+__device__ __forceinline__ float row_min(float v) { return row_fold(v, low); }
 template <typename F>
 __device__ __forceinline__ F row_add(F v) {
   return row_fold(v, [](F a, F b) { return a + b; });
