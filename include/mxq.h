@@ -719,10 +719,12 @@ typedef enum { MXQ_SOFTMAX = 0, MXQ_SIGMOID = 1 } mxq_score;
  *               dropped by mxq_sort_experts)
  *   weights     [n_tokens, top_k] fp32: scale * score, or with renormalize scale * score / the sum
  *               of the chosen scores; 0 for an id of -1
+ * Weights and gradients are computed in fp32 at least.
  * A NaN key counts as the smallest of those that are open; weights of such a token may be NaN.
  * 1 <= top_k <= top_groups * (n_experts / n_groups), n_experts <= 512, scale finite.
  * mxq_route_experts_backward: the gradient of the logits for dweights [n_tokens, top_k], the
- * choice held fixed (the bias has no gradient); slots whose id is not an expert's count nothing.
+ * choice held fixed (the bias has no gradient); slots whose id is not an expert's count nothing, and a
+ * token without any other has gradient 0, whatever its logits are.
  *   dlogits     [n_tokens, n_experts] of the logits' type, row stride ld_dlogits >= n_experts
  */
 int mxq_route_experts(const void* logits, int64_t ld_logits, int64_t n_tokens, int64_t n_experts, mxq_dtype dt,

@@ -239,7 +239,8 @@ __device__ __forceinline__ f32x8 gradient_at(const ActArgs& s, int64_t r, int c)
 }
 
 // What a workgroup takes: the same 128 columns of both halves, which reads them once; or 128 columns of the result, which
-// lie in one of the halves or across their border.
+// lie in one of the halves or across their border.  The latter, where F is no multiple of 128, reads gate and da twice and
+// takes the exponentials twice: 16000 x 1000 bf16 53.0 us, of 1024 columns 35.1.
 enum Part { kBothHalves, kGateHalf, kUpHalf, kBorder };
 
 template <typename T, int kAct, bool kVec, bool kStream, Part kPart, bool kWhole, int kRows>

@@ -11,9 +11,15 @@
 //              where the weights sum to scale, p_j h_j = w_j (g_j - sum g w / scale), for both,
 //              and sum h p = 0
 //
-// Instructions bound the choice, about 1250 a wave of four tokens, most of them comparisons in pairs: 16384 fp32 tokens of 256
-// experts with a bias and 8 groups 14.0 us, 131072 of them 63.6 (2.2 TB/s); 131072 bf16 tokens of 128 experts 27.5.
-// Gradients of 131072 bf16 tokens of 128 experts take 23.9 us, 6.0 TB/s.
+// Choices need 64 bits, weights and gradients do not: where sixteen lanes share a token they are computed in fp32, the weights
+// off by 6e-8 of themselves in the root mean square and by up to 4e-7; where a wave has it in 64 bits (2.5e-8, 6e-8).
+//
+// Instructions bound the choice, 1259 a wave of four fp32 tokens of 256 experts with a bias and 8 groups, most of them
+// comparisons in pairs: 131072 tokens take 64 us (2.2 TB/s) with 94% of the issue slots taken; 16384 are one round of waves,
+// 14.0 us and 39%.  131072 bf16 tokens of 128 experts take 26.3 us (596 instructions a wave, 94%).  A wave that has a token
+// to itself takes 1235: 65536 fp32 tokens of 128 experts, 20 of them chosen, 115 us, all slots taken.  Gradients of 131072
+// tokens of 128 experts take 23.5 us in fp32 (6.1 TB/s) and 15.8 in bf16 (4.8); for 65536 fp32 tokens of 20 choices, a wave
+// each in 64 bits, 65.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -171,7 +177,8 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, const WaveLds& s
   wave_sync();
 }
 
-// kOwn experts a lane: lane + 64 i.  4096 fp32 tokens of 128 experts, 20 of them chosen: 11.4 us.
+// kOwn experts a lane: lane + 64 i.  4096 fp32 tokens of 128 experts, 20 of them chosen: 11.4 us.  Each choice is a fold of the
+// whole wave, one after the other.
 template <bool kBf16, int kOwn>
 __device__ void route_exact(const RouteArgs& a, int64_t token, char* lds) {
   const WaveLds sh(lds, a);
